@@ -414,6 +414,86 @@ mlstm_status slstm_fwd(const float *x_pre, const void *R, int B, int NH, int S, 
                        void *h_out, float *c_final, float *n_final, float *m_final, float *h_final,
                        void *stream);
 
+/*
+ * The operators below surround the cells in a block: the residual addition and
+ * norm that opens it, the short causal convolution in front of the cell, and the
+ * selective state space recurrence, a cell with one decay per channel and state.
+ *
+ * Conventions they share
+ *   - Activations are rows of D (d for the norm) contiguous elements; consecutive
+ *     rows are `*_stride` elements apart (>= the row's width), so a column range of
+ *     a wider projection is passed as it is.  Any element alignment is accepted.
+ *   - A batch is B sequences.  With seq_start NULL they are S rows each, sequence b
+ *     at rows b*S .. b*S + S - 1 (rows = B*S).  With seq_start they are packed:
+ *     seq_start[0..B] (int32, in device memory, ascending) gives sequence b the rows
+ *     seq_start[b] .. seq_start[b+1] - 1 of `rows` rows, S is the length of the
+ *     longest, and a sequence may be empty.  The kernels clamp the entries to
+ *     [0, rows] and a length to S, so no entry makes them leave the tensors; rows
+ *     that belong to no sequence are neither read nor written.
+ *   - Parameters, states and their gradients are fp32; gradients of activations have
+ *     the activations' dtype (sums run in fp32 and are rounded once).
+ *   - Outputs may not share bytes with inputs or each other except where said.
+ *     Column ranges of one buffer with the same row stride do not count as sharing.
+ *   - No atomics: repeated calls on the same inputs give the same bits.
+ */
+typedef enum ssm_act {
+    SSM_ACT_NONE = 0,
+    SSM_ACT_SWISH = 1            /* p * sigmoid(p) */
+} ssm_act;
+
+/*
+ * Residual addition and root-mean-square norm.  Per row:
+ *   r = x + residual, rounded to res_dtype (residual NULL: r = x, so rounded)
+ *   y = weight r / sqrt(mean(r^2) + eps)
+ * The norm is taken of the rounded r, the one that residual_out holds and the
+ * backward reads.
+ *   x [rows,d] dtype;  residual [rows,d] res_dtype or NULL;  weight [d] fp32
+ *   residual_out [rows,d] res_dtype, dense, or NULL (not wanted); may be the buffer
+ *   of residual or x where that has the same stride and dtype
+ *   y_out [rows,d] dtype, dense
+ *   rows >= 1; 1 <= d <= 16384; eps finite, >= 0 (a row of zeros needs eps > 0)
+ */
+mlstm_status mlstm_rms_norm_fwd(const void *x, long long x_stride,
+                                const void *residual, long long residual_stride,
+                                const float *weight, int rows, int d, float eps,
+                                mlstm_dtype dtype, mlstm_dtype res_dtype,
+                                void *residual_out, void *y_out, void *stream);
+
+/*
+ * The same with y in 8 bits: per row and group of `group` columns (32, 64 or 128;
+ * 0 = the whole row; the last group may be shorter)
+ *   scale = max |y| / 448,   q = e4m3(y / scale)   (round to nearest even)
+ * and q = 0, scale = 0 where the group's y are all zero.
+ *   q_out [rows,d] one OCP e4m3 byte per element, dense
+ *   scale_out [rows, ceil(d/group)] fp32, dense
+ */
+mlstm_status mlstm_rms_norm_quant(const void *x, long long x_stride,
+                                  const void *residual, long long residual_stride,
+                                  const float *weight, int rows, int d, float eps,
+                                  mlstm_dtype dtype, mlstm_dtype res_dtype, int group,
+                                  void *residual_out, void *q_out, float *scale_out,
+                                  void *stream);
+
+/*
+ * Backward of the norm from r, the sum it was taken of.  With v = weight dy,
+ * k = 1 / sqrt(mean(r^2) + eps):
+ *   dr = k (v - r k^2 mean(v r)) + dres;   dweight = sum over rows of dy r k
+ * dr is the gradient of x and of residual alike.
+ *   r [rows,d] res_dtype (residual_out of the forward);  dy [rows,d] dtype
+ *   dres [rows,d] res_dtype, dense: gradient that reaches r by other ways, or NULL
+ *   grad_x [rows,d] dtype, dense, or NULL;  grad_residual [rows,d] res_dtype, dense,
+ *   or NULL (one of the two at least); grad_residual may be the buffer of dres
+ *   grad_weight [d] fp32
+ *   workspace: mlstm_rms_norm_bwd_workspace_bytes(rows, d) bytes, 4-byte aligned
+ */
+size_t mlstm_rms_norm_bwd_workspace_bytes(int rows, int d);
+mlstm_status mlstm_rms_norm_bwd(const void *r, long long r_stride, const float *weight,
+                                const void *dy, long long dy_stride, const void *dres,
+                                int rows, int d, float eps,
+                                mlstm_dtype dtype, mlstm_dtype res_dtype,
+                                void *grad_x, void *grad_residual, float *grad_weight,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
 /* Static description of a status code. */
 const char *mlstm_status_string(mlstm_status status);
 

@@ -17,6 +17,9 @@ Entry points (same names as include/mlstm.h):
                       the forward and the block epilogue in one call (fused where a
                       workgroup holds a head's whole rows)
   slstm_fwd           the sLSTM recurrence with block-diagonal (per-head) memory mixing
+  mlstm_rms_norm_fwd, mlstm_rms_norm_quant, mlstm_rms_norm_bwd
+                      residual addition and root-mean-square norm, the same with an e4m3 output
+                      and scales, and the backward
   mlstm_fwd_workspace_bytes, mlstm_status_string, mlstm_error_detail
 """
 from .binding import (  # noqa: F401
@@ -44,4 +47,8 @@ from .binding import (  # noqa: F401
     mlstm_status_string,
     mlstm_step,
     slstm_fwd,
+    mlstm_rms_norm_bwd,
+    mlstm_rms_norm_bwd_workspace_bytes,
+    mlstm_rms_norm_fwd,
+    mlstm_rms_norm_quant,
 )

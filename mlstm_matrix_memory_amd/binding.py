@@ -53,6 +53,7 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     import torch  # noqa: F401  (loads torch's HIP runtime before the library's dependency is resolved)
     lib = ctypes.CDLL(path)
     vp, fp, i, sz = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    ll, f = ctypes.c_longlong, ctypes.c_float
     lib.mlstm_fwd_workspace_bytes.restype = sz
     lib.mlstm_fwd_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
     lib.mlstm_fwd_parallel.restype = i
@@ -87,6 +88,14 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     lib.slstm_fwd.argtypes = [fp, vp, i, i, i, i, i, i, fp, fp, fp, fp, vp, fp, fp, fp, fp, vp]
     lib.mlstm_step.restype = i
     lib.mlstm_step.argtypes = [vp, vp, vp, fp, fp, fp, i, i, i, i, i, fp, fp, fp, vp, vp]
+    lib.mlstm_rms_norm_fwd.restype = i
+    lib.mlstm_rms_norm_fwd.argtypes = [vp, ll, vp, ll, vp, i, i, f, i, i, vp, vp, vp]
+    lib.mlstm_rms_norm_quant.restype = i
+    lib.mlstm_rms_norm_quant.argtypes = [vp, ll, vp, ll, vp, i, i, f, i, i, i, vp, vp, vp, vp]
+    lib.mlstm_rms_norm_bwd_workspace_bytes.restype = sz
+    lib.mlstm_rms_norm_bwd_workspace_bytes.argtypes = [i, i]
+    lib.mlstm_rms_norm_bwd.restype = i
+    lib.mlstm_rms_norm_bwd.argtypes = [vp, ll, vp, vp, ll, vp, i, i, f, i, i, vp, vp, vp, vp, sz, vp]
     lib.mlstm_status_string.restype = ctypes.c_char_p
     lib.mlstm_status_string.argtypes = [i]
     lib.mlstm_error_detail.restype = ctypes.c_char_p
@@ -100,7 +109,7 @@ def header_symbols(path: str = HEADER) -> list[str]:
     """Names of the functions include/mlstm.h declares."""
     text = open(path).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return sorted(set(re.findall(r"\b((?:mlstm|slstm)_[a-z_0-9]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b((?:mlstm|slstm|ssm)_[a-z_0-9]+)\s*\(", text)))
 
 
 def mlstm_status_string(status: int) -> str:
@@ -557,3 +566,204 @@ def mlstm_step(q, k, v, i_pre, f_pre, o_pre, C, n, m, h_out=None, stream=None):
     if st != MLSTM_OK:
         raise MlstmError("mlstm_step", st, mlstm_error_detail())
     return h_out
+
+
+# ---- operators around the cells: norm, short convolution, selective scan ---------------
+#
+# Their activations are rows (leading dimensions) of contiguous elements; rows may be
+# any uniform distance apart, so a column range of a wider projection is passed as is.
+
+def _row_stride(t, name, trailing: int = 1) -> int:
+    """Distance in elements between consecutive rows of t; its last `trailing`
+    dimensions make a row, which must be contiguous."""
+    width = 1
+    if t.is_contiguous():
+        for k in t.shape[t.dim() - trailing:]:
+            width *= k
+        return width
+    shape, stride = t.shape, t.stride()
+    for k in range(t.dim() - 1, t.dim() - trailing - 1, -1):
+        if shape[k] != 1 and stride[k] != width:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        width *= shape[k]
+    step = None
+    for k in range(t.dim() - trailing - 1, -1, -1):
+        if shape[k] == 1:
+            continue
+        if step is None:
+            step, expect = stride[k], stride[k] * shape[k]
+        elif stride[k] != expect:
+            raise ValueError(f"the rows of {name} must be a uniform distance apart")
+        else:
+            expect *= shape[k]
+    return width if step is None else step
+
+
+def _check_rows(t, name, shape, dtype, device):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _gpu(t, name):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must live on a GPU")
+    return t.device
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(name, dev, *args):
+    """Calls the C entry point with the tensors' device current; raises on a status."""
+    import torch
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args)
+    if st != MLSTM_OK:
+        raise MlstmError(name, st, mlstm_error_detail())
+
+
+def _workspace(workspace, need, dev, owned):
+    """(tensor, pointer, bytes) of the given workspace or of one allocated here."""
+    import torch
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        owned.append(workspace)
+    if workspace is None:
+        return None, 0
+    if workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _output(t, name, shape, dtype, dev, owned):
+    """The given output, checked, or a dense one allocated here."""
+    import torch
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        owned.append(t)
+    else:
+        _check_rows(t, name, shape, dtype, dev)
+    return t
+
+
+def mlstm_rms_norm_bwd_workspace_bytes(rows: int, d: int) -> int:
+    return int(load_library().mlstm_rms_norm_bwd_workspace_bytes(rows, d))
+
+
+def _norm_inputs(x, weight, residual, residual_out, owned):
+    import torch
+    dev, d = _gpu(x, "x"), x.shape[-1]
+    _dtype_code(x)
+    _check(weight, "weight", (d,), torch.float32, dev)
+    res_dtype = x.dtype
+    if residual is not None:
+        _dtype_code(residual)
+        res_dtype = residual.dtype
+        _check_rows(residual, "residual", x.shape, res_dtype, dev)
+        if residual_out is None:
+            residual_out = torch.empty(x.shape, dtype=res_dtype, device=dev)
+            owned.append(residual_out)
+    elif residual_out is not None:
+        res_dtype = residual_out.dtype
+    if residual_out is not None:
+        _check(residual_out, "residual_out", x.shape, res_dtype, dev)
+        _dtype_code(residual_out)
+    code = MLSTM_F32 if res_dtype == torch.float32 else MLSTM_BF16
+    rows = x.numel() // d if d else 0
+    return (x.data_ptr(), _row_stride(x, "x"), _ptr(residual),
+            0 if residual is None else _row_stride(residual, "residual"), weight.data_ptr(), rows, d), code, residual_out, dev
+
+
+def mlstm_rms_norm_fwd(x, weight, residual=None, eps: float = 1e-5, residual_out=None, y_out=None, stream=None):
+    """Residual addition and root-mean-square norm over the last dimension; returns (y, r).
+
+    x [..., d] float32 or bfloat16; weight [d] float32; residual like x, float32 or
+    bfloat16 on its own.  r = x + residual in the residual's dtype is allocated when
+    not given (residual_out may be residual itself); without a residual r is x.
+    """
+    import torch
+    owned = []
+    head, res_code, residual_out, dev = _norm_inputs(x, weight, residual, residual_out, owned)
+    if y_out is None:
+        y_out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        owned.append(y_out)
+    _check(y_out, "y_out", x.shape, x.dtype, dev)
+    _keep_for_stream(stream, dev, owned)
+    _launch("mlstm_rms_norm_fwd", dev, *head, float(eps), _dtype_code(x), res_code, _ptr(residual_out),
+            y_out.data_ptr(), _stream_handle(stream, dev))
+    return y_out, x if residual_out is None else residual_out
+
+
+def mlstm_rms_norm_quant(x, weight, residual=None, eps: float = 1e-5, group: int = 0, residual_out=None, q_out=None,
+                         scale_out=None, stream=None):
+    """mlstm_rms_norm_fwd with an e4m3 output; returns (q, scale, r).
+
+    y is q * scale with one scale per row and group of 32, 64 or 128 columns (0: per
+    row): q like x in torch.float8_e4m3fn, scale [..., ceil(d/group)] float32.
+    """
+    import torch
+    owned = []
+    head, res_code, residual_out, dev = _norm_inputs(x, weight, residual, residual_out, owned)
+    d, group = x.shape[-1], int(group)
+    per_row = -(-d // group) if group > 0 else 1
+    if q_out is None:
+        q_out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+        owned.append(q_out)
+    if scale_out is None:
+        scale_out = torch.empty((*x.shape[:-1], per_row), dtype=torch.float32, device=dev)
+        owned.append(scale_out)
+    _check(q_out, "q_out", x.shape, torch.float8_e4m3fn, dev)
+    _check(scale_out, "scale_out", (*x.shape[:-1], per_row), torch.float32, dev)
+    _keep_for_stream(stream, dev, owned)
+    _launch("mlstm_rms_norm_quant", dev, *head, float(eps), _dtype_code(x), res_code, group, _ptr(residual_out),
+            q_out.data_ptr(), scale_out.data_ptr(), _stream_handle(stream, dev))
+    return q_out, scale_out, x if residual_out is None else residual_out
+
+
+def mlstm_rms_norm_bwd(r, weight, dy, dres=None, eps: float = 1e-5, grad_x=None, grad_residual=None,
+                       grad_weight=None, workspace=None, stream=None):
+    """Backward of mlstm_rms_norm_fwd; returns (grad_x, grad_residual, grad_weight).
+
+    r [..., d]: the sum the norm was taken of; dy like the norm's output, its dtype the
+    dtype of grad_x; dres like r: gradient that reaches the sum by other ways.  Where
+    both dtypes are equal grad_residual is grad_x unless it is given.
+    """
+    import torch
+    dev, d = _gpu(r, "r"), r.shape[-1]
+    res_code, code = _dtype_code(r), _dtype_code(dy)
+    _check(weight, "weight", (d,), torch.float32, dev)
+    _check_rows(dy, "dy", r.shape, dy.dtype, dev)
+    if dres is not None:
+        _check(dres, "dres", r.shape, r.dtype, dev)
+    owned = []
+    if grad_x is None:
+        grad_x = torch.empty(r.shape, dtype=dy.dtype, device=dev)
+        owned.append(grad_x)
+    if grad_residual is None and r.dtype != dy.dtype:
+        grad_residual = torch.empty(r.shape, dtype=r.dtype, device=dev)
+        owned.append(grad_residual)
+    if grad_weight is None:
+        grad_weight = torch.empty((d,), dtype=torch.float32, device=dev)
+        owned.append(grad_weight)
+    _check(grad_x, "grad_x", r.shape, dy.dtype, dev)
+    if grad_residual is not None:
+        _check(grad_residual, "grad_residual", r.shape, r.dtype, dev)
+    _check(grad_weight, "grad_weight", (d,), torch.float32, dev)
+    rows = r.numel() // d if d else 0
+    ws, ws_bytes = _workspace(workspace, mlstm_rms_norm_bwd_workspace_bytes(rows, d), dev, owned)
+    _keep_for_stream(stream, dev, owned)
+    _launch("mlstm_rms_norm_bwd", dev, r.data_ptr(), _row_stride(r, "r"), weight.data_ptr(), dy.data_ptr(),
+            _row_stride(dy, "dy"), _ptr(dres), rows, d, float(eps), code, res_code, grad_x.data_ptr(),
+            _ptr(grad_residual), grad_weight.data_ptr(), ws, ws_bytes, _stream_handle(stream, dev))
+    return grad_x, grad_x if grad_residual is None else grad_residual, grad_weight

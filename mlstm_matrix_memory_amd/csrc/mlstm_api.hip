@@ -10,8 +10,10 @@
 #include "mlstm_internal.h"
 
 namespace {
-
 thread_local char g_detail[512] = "";
+}
+
+namespace mlstm {
 
 mlstm_status fail(mlstm_status s, const char* fmt, ...) {
     va_list ap;
@@ -25,6 +27,13 @@ mlstm_status ok() {
     g_detail[0] = '\0';
     return MLSTM_OK;
 }
+
+}  // namespace mlstm
+
+namespace {
+
+using mlstm::fail;
+using mlstm::ok;
 
 constexpr int MAX_DIM = 4096;
 

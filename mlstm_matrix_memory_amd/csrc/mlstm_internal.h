@@ -102,6 +102,10 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+// ---- status of an entry point (kept per thread for mlstm_error_detail) -----
+mlstm_status fail(mlstm_status s, const char* fmt, ...);
+mlstm_status ok();
+
 // ---- launchers (return hipSuccess or the launch error) --------------------
 struct FwdArgs {
     const void* q; const void* k; const void* v;

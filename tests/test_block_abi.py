@@ -1,0 +1,85 @@
+"""Argument validation of the block operators on the CPU: every refusal happens before
+any HIP call, with a status and a reason."""
+import pytest
+
+from mlstm_matrix_memory_amd import binding as b
+
+P = [0x10000000 * (k + 1) for k in range(32)]     # far apart, aligned, never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return b.load_library()
+
+
+def refused(status, words, code=b.MLSTM_ERR_INVALID_ARG):
+    assert status == code, (status, b.mlstm_error_detail())
+    assert words in b.mlstm_error_detail()
+
+
+def _norm(lib, quant=False, **kw):
+    a = dict(x=P[0], xs=64, res=P[1], rs=64, w=P[2], rows=4, d=64, eps=1e-5, dt=1, rdt=0, group=0, rout=P[3], y=P[4],
+             scale=P[5])
+    a.update(kw)
+    head = (a["x"], a["xs"], a["res"], a["rs"], a["w"], a["rows"], a["d"], a["eps"], a["dt"], a["rdt"])
+    if quant:
+        return lib.mlstm_rms_norm_quant(*head, a["group"], a["rout"], a["y"], a["scale"], None)
+    return lib.mlstm_rms_norm_fwd(*head, a["rout"], a["y"], None)
+
+
+NORM_BAD = [
+    (dict(rows=0), "rows=0"), (dict(d=0), "d=0"), (dict(d=16385, xs=16385, rs=16385), "d=16385"),
+    (dict(eps=-1.0), "eps=-1"), (dict(eps=float("nan")), "eps=nan"), (dict(eps=float("inf")), "eps=inf"),
+    (dict(dt=2), "dtype=2"), (dict(rdt=5), "res_dtype=5"),
+    (dict(x=None), "x is NULL"), (dict(w=None), "weight is NULL"), (dict(x=P[0] + 1), "x is not 2-byte aligned"),
+    (dict(rout=P[3] + 2), "residual_out is not 4-byte aligned"),
+    (dict(xs=63), "x_stride=63"), (dict(rs=-64), "residual_stride"),
+    (dict(rout=P[1] + 4), "residual_out overlaps residual"), (dict(rout=P[0]), "overlaps"),
+]
+
+
+@pytest.mark.parametrize("kw,words", NORM_BAD + [(dict(y=None), "y_out is NULL"), (dict(y=P[0]), "y_out overlaps x")])
+def test_norm_refusals(lib, kw, words):
+    if "rout" in kw and kw["rout"] == P[0]:
+        words = "residual_out overlaps x"
+    refused(_norm(lib, **kw), words)
+
+
+@pytest.mark.parametrize("kw,words", NORM_BAD + [
+    (dict(group=16), "group=16"), (dict(group=-32), "group=-32"), (dict(y=None), "q_out is NULL"),
+    (dict(scale=None), "scale_out is NULL"), (dict(scale=P[4] + 4), "overlaps")])
+def test_norm_quant_refusals(lib, kw, words):
+    refused(_norm(lib, quant=True, **kw), words)
+
+
+def _norm_bwd(lib, **kw):
+    a = dict(r=P[0], rs=64, w=P[1], dy=P[2], ds=64, dres=P[3], rows=4, d=64, eps=1e-5, dt=1, rdt=0, gx=P[4], gr=P[5],
+             gw=P[6], ws=P[7], n=1 << 20)
+    a.update(kw)
+    return lib.mlstm_rms_norm_bwd(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,words", [
+    (dict(rows=-1), "rows=-1"), (dict(d=0), "d=0"), (dict(r=None), "r is NULL"), (dict(dy=None), "dy is NULL"),
+    (dict(gw=None), "grad_weight is NULL"), (dict(gx=None, gr=None), "both NULL"), (dict(ds=5), "dy_stride=5"),
+    (dict(gx=P[2]), "grad_x overlaps dy"), (dict(gr=P[0]), "grad_residual overlaps r"), (dict(gx=P[3]), "overlaps"),
+    (dict(gw=P[7] + 64), "overlaps"), (dict(ws=P[7] + 2), "workspace is not 4-byte aligned"),
+])
+def test_norm_bwd_refusals(lib, kw, words):
+    refused(_norm_bwd(lib, **kw), words)
+
+
+def test_norm_bwd_workspace(lib):
+    need = b.mlstm_rms_norm_bwd_workspace_bytes(4, 64)
+    assert need >= 64 * 4
+    refused(_norm_bwd(lib, n=need - 1), "needed", b.MLSTM_ERR_WORKSPACE)
+    refused(_norm_bwd(lib, ws=None), "needed", b.MLSTM_ERR_WORKSPACE)
+    assert b.mlstm_rms_norm_bwd_workspace_bytes(0, 64) == 0
+    assert b.mlstm_rms_norm_bwd_workspace_bytes(4, 20000) == 0
+
+
+def test_block_operators_exported(lib):
+    import mlstm_matrix_memory_amd as pkg
+    for name in ("mlstm_rms_norm_fwd", "mlstm_rms_norm_quant", "mlstm_rms_norm_bwd",
+                 "mlstm_rms_norm_bwd_workspace_bytes"):
+        assert name in b.header_symbols() and hasattr(lib, name) and callable(getattr(pkg, name))

@@ -1,0 +1,41 @@
+"""The fp64 references of the block operators against their own definitions: gradients
+against differences of the forward, special cases against closed forms (CPU)."""
+import numpy as np
+import pytest
+
+import block_reference as ref
+
+
+def difference(f, args, k, i, weight, h=1e-6):
+    """Central difference of sum(weight * f(args)) along element i of args[k]."""
+    out = []
+    for s in (h, -h):
+        a = [np.array(x, np.float64) if x is not None else None for x in args]
+        a[k].reshape(-1)[i] += s
+        out.append(sum(float((w * y).sum()) for w, y in zip(weight, f(*a))))
+    return (out[0] - out[1]) / (2 * h)
+
+
+@pytest.mark.parametrize("d", [1, 5, 32])
+def test_norm_gradients_are_differences(d):
+    rng = np.random.default_rng(d)
+    r, w, dy = rng.standard_normal((3, d)), rng.standard_normal(d), rng.standard_normal((3, d))
+    dres = rng.standard_normal((3, d))
+    dr, dw = ref.norm_bwd(r, w, dy, dres, 1e-3)
+    for k, grad in ((0, dr - dres), (1, dw)):
+        for i in range(grad.size):
+            got = difference(lambda a, b: (ref.norm_fwd(a, b, 1e-3),), (r, w), k, i, (dy,))
+            assert abs(got - grad.reshape(-1)[i]) <= 1e-7 * (1 + abs(got))
+
+
+def test_norm_of_equal_values_is_the_weight():
+    w = np.array([1.0, -2.0, 0.5])
+    assert np.allclose(ref.norm_fwd(np.full((2, 3), 7.0), w, 0.0), w, atol=1e-15)
+    assert np.array_equal(ref.norm_fwd(np.zeros((1, 3)), w, 1e-5), np.zeros((1, 3)))
+
+
+def test_group_scales():
+    y = np.arange(-10.0, 11.0)[None]
+    scale, wide = ref.quantise_groups(y, 8)
+    assert np.allclose(scale * 448, [[10, 5, 10]]) and wide.shape == y.shape
+    assert np.allclose(ref.quantise_groups(y, 0)[0] * 448, [[10]])
