@@ -494,6 +494,46 @@ mlstm_status mlstm_rms_norm_bwd(const void *r, long long r_stride, const float *
                                 void *grad_x, void *grad_residual, float *grad_weight,
                                 void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Short causal depthwise convolution (the block's "causal conv" of window 4 with
+ * swish in front of the cell).  Per channel d, row t of a sequence:
+ *   p_t = bias[d] + sum_{j < width} weight[d][j] x_{t - width + 1 + j}
+ *   y_t = p_t (SSM_ACT_NONE) or p_t sigmoid(p_t) (SSM_ACT_SWISH)
+ * Rows before the first are state_init's, or zero.
+ *   x [rows,D] dtype;  weight [D,width];  bias [D] or NULL;  width 2, 3 or 4
+ *   state_init [B,width-1,D] dtype, dense, or NULL: the inputs before row 0, oldest first
+ *   y_out [rows,D] dtype;  state_final like state_init, or NULL: the last width - 1
+ *   inputs (those of state_init among them where a sequence is shorter)
+ */
+mlstm_status ssm_conv_fwd(const void *x, long long x_stride, const float *weight, const float *bias,
+                          const int *seq_start, const void *state_init,
+                          int B, int S, int rows, int D, int width, ssm_act act, mlstm_dtype dtype,
+                          void *y_out, long long y_stride, void *state_final, void *stream);
+
+/*
+ * One row of the convolution for each of B sequences (x, y_out [B,D]); state
+ * [B,width-1,D] is shifted in place.
+ */
+mlstm_status ssm_conv_step(const void *x, long long x_stride, const float *weight, const float *bias,
+                           int B, int D, int width, ssm_act act, mlstm_dtype dtype,
+                           void *state, void *y_out, long long y_stride, void *stream);
+
+/*
+ * Backward of ssm_conv_fwd, from its inputs and dy [rows,D] dtype.
+ *   dstate_final [B,width-1,D] dtype or NULL: gradient of state_final
+ *   grad_x [rows,D] dtype;  grad_weight [D,width];  grad_bias [D] (NULL if bias is)
+ *   grad_state_init [B,width-1,D] dtype, or NULL (not wanted)
+ *   workspace: ssm_conv_bwd_workspace_bytes(...) bytes, 4-byte aligned
+ */
+size_t ssm_conv_bwd_workspace_bytes(int B, int S, int D, int width);
+mlstm_status ssm_conv_bwd(const void *x, long long x_stride, const float *weight, const float *bias,
+                          const int *seq_start, const void *state_init,
+                          const void *dy, long long dy_stride, const void *dstate_final,
+                          int B, int S, int rows, int D, int width, ssm_act act, mlstm_dtype dtype,
+                          void *grad_x, long long grad_x_stride, float *grad_weight, float *grad_bias,
+                          void *grad_state_init,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
 /* Static description of a status code. */
 const char *mlstm_status_string(mlstm_status status);
 

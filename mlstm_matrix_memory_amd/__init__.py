@@ -20,6 +20,9 @@ Entry points (same names as include/mlstm.h):
   mlstm_rms_norm_fwd, mlstm_rms_norm_quant, mlstm_rms_norm_bwd
                       residual addition and root-mean-square norm, the same with an e4m3 output
                       and scales, and the backward
+  ssm_conv_fwd, ssm_conv_step, ssm_conv_bwd
+                      short causal depthwise convolution with swish, for sequences and for
+                      single rows, and its backward
   mlstm_fwd_workspace_bytes, mlstm_status_string, mlstm_error_detail
 """
 from .binding import (  # noqa: F401
@@ -51,4 +54,10 @@ from .binding import (  # noqa: F401
     mlstm_rms_norm_bwd_workspace_bytes,
     mlstm_rms_norm_fwd,
     mlstm_rms_norm_quant,
+    SSM_ACT_NONE,
+    SSM_ACT_SWISH,
+    ssm_conv_bwd,
+    ssm_conv_bwd_workspace_bytes,
+    ssm_conv_fwd,
+    ssm_conv_step,
 )

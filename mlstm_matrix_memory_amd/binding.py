@@ -96,6 +96,15 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     lib.mlstm_rms_norm_bwd_workspace_bytes.argtypes = [i, i]
     lib.mlstm_rms_norm_bwd.restype = i
     lib.mlstm_rms_norm_bwd.argtypes = [vp, ll, vp, vp, ll, vp, i, i, f, i, i, vp, vp, vp, vp, sz, vp]
+    lib.ssm_conv_fwd.restype = i
+    lib.ssm_conv_fwd.argtypes = [vp, ll, vp, vp, vp, vp, i, i, i, i, i, i, i, vp, ll, vp, vp]
+    lib.ssm_conv_step.restype = i
+    lib.ssm_conv_step.argtypes = [vp, ll, vp, vp, i, i, i, i, i, vp, vp, ll, vp]
+    lib.ssm_conv_bwd_workspace_bytes.restype = sz
+    lib.ssm_conv_bwd_workspace_bytes.argtypes = [i, i, i, i]
+    lib.ssm_conv_bwd.restype = i
+    lib.ssm_conv_bwd.argtypes = [vp, ll, vp, vp, vp, vp, vp, ll, vp, i, i, i, i, i, i, i, vp, ll, vp, vp, vp, vp, sz,
+                                 vp]
     lib.mlstm_status_string.restype = ctypes.c_char_p
     lib.mlstm_status_string.argtypes = [i]
     lib.mlstm_error_detail.restype = ctypes.c_char_p
@@ -767,3 +776,110 @@ def mlstm_rms_norm_bwd(r, weight, dy, dres=None, eps: float = 1e-5, grad_x=None,
             _row_stride(dy, "dy"), _ptr(dres), rows, d, float(eps), code, res_code, grad_x.data_ptr(),
             _ptr(grad_residual), grad_weight.data_ptr(), ws, ws_bytes, _stream_handle(stream, dev))
     return grad_x, grad_x if grad_residual is None else grad_residual, grad_weight
+
+
+SSM_ACT_NONE = 0
+SSM_ACT_SWISH = 1
+
+
+def _batch(x, seq_start, max_len, dev):
+    """(B, S, rows) of a batch: x [B, S, D], or packed sequences x [rows, D]."""
+    import torch
+    if seq_start is None:
+        if x.dim() != 3:
+            raise ValueError("x must be 3-D [B, S, D] (2-D [rows, D] with seq_start)")
+        return x.shape[0], x.shape[1], x.shape[0] * x.shape[1]
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [rows, D] with seq_start")
+    if seq_start.dim() != 1 or seq_start.numel() < 2:
+        raise ValueError("seq_start must be 1-D with a start per sequence and the last one's end")
+    _check(seq_start, "seq_start", (seq_start.numel(),), torch.int32, dev)
+    if max_len is None:
+        raise ValueError("seq_start needs max_len, the length of the longest sequence")
+    return seq_start.numel() - 1, int(max_len), x.shape[0]
+
+
+def ssm_conv_fwd(x, weight, bias=None, act: int = SSM_ACT_SWISH, state_init=None, seq_start=None, max_len=None,
+                 y_out=None, state_final=None, stream=None):
+    """Short causal depthwise convolution; returns (y, state_final).
+
+    x [B,S,D] (or packed [rows,D] with seq_start int32 [B+1] and max_len) float32 or
+    bfloat16; weight [D,width] and bias [D] float32, width 2 to 4; state_init
+    [B,width-1,D] like x: the inputs before each sequence's first (None = zero).
+    """
+    import torch
+    dev, dt = _gpu(x, "x"), _dtype_code(x)
+    B, S, rows = _batch(x, seq_start, max_len, dev)
+    D, W = x.shape[-1], weight.shape[-1]
+    _check(weight, "weight", (D, W), torch.float32, dev)
+    if bias is not None:
+        _check(bias, "bias", (D,), torch.float32, dev)
+    if state_init is not None:
+        _check(state_init, "state_init", (B, W - 1, D), x.dtype, dev)
+    owned = []
+    y_out = _output(y_out, "y_out", x.shape, x.dtype, dev, owned)
+    state_final = _output(state_final, "state_final", (B, max(W - 1, 0), D), x.dtype, dev, owned)
+    _check(state_final, "state_final", (B, max(W - 1, 0), D), x.dtype, dev)
+    _keep_for_stream(stream, dev, owned)
+    _launch("ssm_conv_fwd", dev, x.data_ptr(), _row_stride(x, "x"), weight.data_ptr(), _ptr(bias), _ptr(seq_start),
+            _ptr(state_init), B, S, rows, D, W, int(act), dt, y_out.data_ptr(), _row_stride(y_out, "y_out"),
+            state_final.data_ptr(), _stream_handle(stream, dev))
+    return y_out, state_final
+
+
+def ssm_conv_step(x, weight, state, bias=None, act: int = SSM_ACT_SWISH, y_out=None, stream=None):
+    """One row of the convolution per sequence: x [B,D]; state [B,width-1,D] is shifted
+    in place.  Returns y [B,D]."""
+    import torch
+    dev, dt = _gpu(x, "x"), _dtype_code(x)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [B, D]")
+    (B, D), W = x.shape, weight.shape[-1]
+    _check(weight, "weight", (D, W), torch.float32, dev)
+    if bias is not None:
+        _check(bias, "bias", (D,), torch.float32, dev)
+    _check(state, "state", (B, W - 1, D), x.dtype, dev)
+    owned = []
+    y_out = _output(y_out, "y_out", x.shape, x.dtype, dev, owned)
+    _keep_for_stream(stream, dev, owned)
+    _launch("ssm_conv_step", dev, x.data_ptr(), _row_stride(x, "x"), weight.data_ptr(), _ptr(bias), B, D, W, int(act),
+            dt, state.data_ptr(), y_out.data_ptr(), _row_stride(y_out, "y_out"), _stream_handle(stream, dev))
+    return y_out
+
+
+def ssm_conv_bwd_workspace_bytes(B: int, S: int, D: int, width: int) -> int:
+    return int(load_library().ssm_conv_bwd_workspace_bytes(B, S, D, width))
+
+
+def ssm_conv_bwd(x, weight, dy, bias=None, act: int = SSM_ACT_SWISH, state_init=None, seq_start=None, max_len=None,
+                 dstate_final=None, grad_x=None, workspace=None, stream=None):
+    """Backward of ssm_conv_fwd; returns (grad_x, grad_weight, grad_bias, grad_state_init).
+
+    Inputs as for the forward, dy like x, dstate_final like state_init.  grad_x is in
+    x's dtype (given, it may be a column range of a wider tensor), the parameters'
+    gradients are float32; those of an absent bias or state_init are None.
+    """
+    import torch
+    dev, dt = _gpu(x, "x"), _dtype_code(x)
+    B, S, rows = _batch(x, seq_start, max_len, dev)
+    D, W = x.shape[-1], weight.shape[-1]
+    _check(weight, "weight", (D, W), torch.float32, dev)
+    if bias is not None:
+        _check(bias, "bias", (D,), torch.float32, dev)
+    for t, name in ((state_init, "state_init"), (dstate_final, "dstate_final")):
+        if t is not None:
+            _check(t, name, (B, W - 1, D), x.dtype, dev)
+    _check_rows(dy, "dy", x.shape, x.dtype, dev)
+    owned = []
+    grad_x = _output(grad_x, "grad_x", x.shape, x.dtype, dev, owned)
+    grad_weight = torch.empty((D, W), dtype=torch.float32, device=dev)
+    grad_bias = None if bias is None else torch.empty((D,), dtype=torch.float32, device=dev)
+    grad_state = None if state_init is None else torch.empty((B, W - 1, D), dtype=x.dtype, device=dev)
+    owned += [grad_weight, grad_bias, grad_state]
+    ws, ws_bytes = _workspace(workspace, ssm_conv_bwd_workspace_bytes(B, S, D, W), dev, owned)
+    _keep_for_stream(stream, dev, owned)
+    _launch("ssm_conv_bwd", dev, x.data_ptr(), _row_stride(x, "x"), weight.data_ptr(), _ptr(bias), _ptr(seq_start),
+            _ptr(state_init), dy.data_ptr(), _row_stride(dy, "dy"), _ptr(dstate_final), B, S, rows, D, W, int(act), dt,
+            grad_x.data_ptr(), _row_stride(grad_x, "grad_x"), grad_weight.data_ptr(), _ptr(grad_bias),
+            _ptr(grad_state), ws, ws_bytes, _stream_handle(stream, dev))
+    return grad_x, grad_weight, grad_bias, grad_state

@@ -61,3 +61,63 @@ def quantise_groups(y, group):
     starts = np.arange(0, d, n)
     scale = np.maximum.reduceat(np.abs(y), starts, axis=-1) / 448.0
     return scale, np.repeat(scale, n, axis=-1)[..., :d]
+
+
+# ---- sequences ---------------------------------------------------------------------
+def sequences(B, S, seq_start=None):
+    """[(first row, one past the last row)] of a batch."""
+    if seq_start is None:
+        return [(b * S, (b + 1) * S) for b in range(B)]
+    return [(int(a), int(z)) for a, z in zip(seq_start[:-1], seq_start[1:])]
+
+
+# ---- short causal convolution ----------------------------------------------------------
+def _sigmoid(x):
+    return 0.5 * (1 + np.tanh(0.5 * x))
+
+
+def conv_fwd(x, weight, bias, state, spans, act):
+    """x [rows,D], state [B,W-1,D]; returns (y [rows,D], final state, sum of |terms| of p)."""
+    x, w, state = (np.asarray(a, np.float64) for a in (x, weight, state))
+    bias = np.zeros(x.shape[1]) if bias is None else np.asarray(bias, np.float64)
+    W = w.shape[1]
+    y, final, size = np.zeros_like(x), state.copy(), np.zeros_like(x)
+    for b, (lo, hi) in enumerate(spans):
+        line = np.concatenate([state[b], x[lo:hi]])
+        n = hi - lo
+        taps = [w[:, j] * line[j:j + n] for j in range(W)]
+        p = bias + sum(taps)
+        size[lo:hi] = np.abs(bias) + sum(np.abs(t) for t in taps)
+        y[lo:hi] = p * _sigmoid(p) if act else p
+        final[b] = line[n:]
+    return y, final, size
+
+
+def conv_bwd(x, weight, bias, state, spans, act, dy, dfinal):
+    """Returns dict of gradients x, weight, bias, state, and of the sums of the absolute
+    values of each one's terms (size_*)."""
+    x, w, state, dy = (np.asarray(a, np.float64) for a in (x, weight, state, dy))
+    bias = np.zeros(x.shape[1]) if bias is None else np.asarray(bias, np.float64)
+    W = w.shape[1]
+    g = {"x": np.zeros_like(x), "weight": np.zeros_like(w), "bias": np.zeros_like(bias), "state": np.zeros_like(state)}
+    g.update({f"size_{k}": np.zeros_like(v) for k, v in g.items()})
+    for b, (lo, hi) in enumerate(spans):
+        line = np.concatenate([state[b], x[lo:hi]])
+        n = hi - lo
+        p = bias + sum(w[:, j] * line[j:j + n] for j in range(W))
+        s = _sigmoid(p)
+        dp = dy[lo:hi] * (s * (1 + p * (1 - s))) if act else dy[lo:hi]
+        dline, size = np.zeros_like(line), np.zeros_like(line)
+        if dfinal is not None:
+            dline[n:] += dfinal[b]
+            size[n:] += np.abs(dfinal[b])
+        for j in range(W):
+            dline[j:j + n] += w[:, j] * dp
+            size[j:j + n] += np.abs(w[:, j] * dy[lo:hi])
+            g["weight"][:, j] += (dp * line[j:j + n]).sum(0)
+            g["size_weight"][:, j] += np.abs(dy[lo:hi] * line[j:j + n]).sum(0)
+        g["bias"] += dp.sum(0)
+        g["size_bias"] += np.abs(dy[lo:hi]).sum(0)
+        g["x"][lo:hi], g["state"][b] = dline[W - 1:], dline[:W - 1]
+        g["size_x"][lo:hi], g["size_state"][b] = size[W - 1:], size[:W - 1]
+    return g

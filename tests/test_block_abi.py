@@ -78,8 +78,77 @@ def test_norm_bwd_workspace(lib):
     assert b.mlstm_rms_norm_bwd_workspace_bytes(4, 20000) == 0
 
 
+def _conv(lib, **kw):
+    a = dict(x=P[0], xs=64, w=P[1], bias=P[2], start=None, init=P[3], B=2, S=8, rows=16, D=64, W=4, act=1, dt=1, y=P[4],
+             ys=64, final=P[5])
+    a.update(kw)
+    return lib.ssm_conv_fwd(*a.values(), None)
+
+
+BATCH_BAD = [
+    (dict(B=0, rows=0), "B=0"), (dict(S=0), "S=0"), (dict(rows=15), "rows=15 is not B*S=16"), (dict(D=0), "D=0"),
+    (dict(start=P[20], S=17), "S=17 exceeds rows=16"), (dict(start=P[20] + 2), "seq_start is not 4-byte aligned"),
+    (dict(dt=7), "dtype=7"), (dict(x=None), "x is NULL"), (dict(xs=63), "x_stride=63"),
+    (dict(x=P[0] + 1), "x is not 2-byte aligned"),
+]
+
+
+@pytest.mark.parametrize("kw,words", BATCH_BAD + [
+    (dict(W=1), "width=1"), (dict(W=5), "width=5"), (dict(act=2), "act=2"), (dict(w=None), "weight is NULL"),
+    (dict(y=None), "y_out is NULL"), (dict(y=P[0]), "y_out overlaps x"), (dict(final=P[3]), "state_final overlaps state_init"),
+    (dict(y=P[0] + 2 * 32, ys=64), "y_out overlaps x"), (dict(start=P[4] + 64), "y_out overlaps seq_start"),
+])
+def test_conv_refusals(lib, kw, words):
+    refused(_conv(lib, **kw), words)
+
+
+def test_too_many_sequences(lib):
+    refused(_conv(lib, B=65536, S=1, rows=65536), "65536", b.MLSTM_ERR_UNSUPPORTED)
+
+
+def test_column_ranges_of_one_buffer_are_apart(lib):
+    # y behind x in rows of one width: accepted so far as to reach the next check
+    refused(_conv(lib, xs=128, y=P[0] + 2 * 64, ys=128, final=P[3]), "state_final overlaps state_init")
+    refused(_conv(lib, xs=127, y=P[0] + 2 * 64, ys=127), "y_out overlaps x")
+
+
+@pytest.mark.parametrize("kw,words", [
+    (dict(B=0), "B=0"), (dict(D=0), "D=0"), (dict(W=5), "width=5"), (dict(state=None), "state is NULL"),
+    (dict(y=P[2]), "overlaps"), (dict(xs=1), "x_stride=1"), (dict(act=-1), "act=-1"), (dict(dt=3), "dtype=3"),
+])
+def test_conv_step_refusals(lib, kw, words):
+    a = dict(x=P[0], xs=64, w=P[1], bias=None, B=2, D=64, W=4, act=1, dt=1, state=P[2], y=P[3], ys=64)
+    a.update(kw)
+    refused(lib.ssm_conv_step(*a.values(), None), words)
+
+
+def _conv_bwd(lib, **kw):
+    a = dict(x=P[0], xs=64, w=P[1], bias=P[2], start=None, init=P[3], dy=P[4], ds=64, df=P[5], B=2, S=8, rows=16, D=64,
+             W=4, act=1, dt=1, gx=P[6], gs=64, gw=P[7], gb=P[8], gi=P[9], ws=P[10], n=1 << 24)
+    a.update(kw)
+    return lib.ssm_conv_bwd(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,words", BATCH_BAD + [
+    (dict(W=0), "width=0"), (dict(dy=None), "dy is NULL"), (dict(gx=None), "grad_x is NULL"),
+    (dict(gw=None), "grad_weight is NULL"), (dict(gb=None), "grad_bias is NULL"),
+    (dict(bias=None), "grad_bias is given without bias"), (dict(gi=P[3]), "grad_state_init overlaps state_init"),
+    (dict(gx=P[4]), "grad_x overlaps dy"), (dict(gw=P[10] + 4), "grad_weight overlaps workspace"),
+])
+def test_conv_bwd_refusals(lib, kw, words):
+    refused(_conv_bwd(lib, **kw), words)
+
+
+def test_conv_bwd_workspace(lib):
+    need = b.ssm_conv_bwd_workspace_bytes(2, 8, 64, 4)
+    assert need >= 5 * 64 * 4
+    refused(_conv_bwd(lib, n=need - 1), "needed", b.MLSTM_ERR_WORKSPACE)
+    assert b.ssm_conv_bwd_workspace_bytes(2, 0, 64, 4) == 0 and b.ssm_conv_bwd_workspace_bytes(2, 8, 64, 9) == 0
+
+
 def test_block_operators_exported(lib):
     import mlstm_matrix_memory_amd as pkg
     for name in ("mlstm_rms_norm_fwd", "mlstm_rms_norm_quant", "mlstm_rms_norm_bwd",
-                 "mlstm_rms_norm_bwd_workspace_bytes"):
+                 "mlstm_rms_norm_bwd_workspace_bytes", "ssm_conv_fwd", "ssm_conv_step", "ssm_conv_bwd",
+                 "ssm_conv_bwd_workspace_bytes"):
         assert name in b.header_symbols() and hasattr(lib, name) and callable(getattr(pkg, name))

@@ -39,3 +39,27 @@ def test_group_scales():
     scale, wide = ref.quantise_groups(y, 8)
     assert np.allclose(scale * 448, [[10, 5, 10]]) and wide.shape == y.shape
     assert np.allclose(ref.quantise_groups(y, 0)[0] * 448, [[10]])
+
+
+@pytest.mark.parametrize("act", [False, True])
+@pytest.mark.parametrize("W", [2, 4])
+def test_conv_gradients_are_differences(W, act):
+    rng = np.random.default_rng(W)
+    start = [0, 3, 3, 4, 9]                       # lengths 3, 0, 1, 5
+    spans = ref.sequences(4, 5, start)
+    x, w, bias = rng.standard_normal((9, 3)), rng.standard_normal((3, W)), rng.standard_normal(3)
+    state, dy, df = rng.standard_normal((4, W - 1, 3)), rng.standard_normal((9, 3)), rng.standard_normal((4, W - 1, 3))
+    g = ref.conv_bwd(x, w, bias, state, spans, act, dy, df)
+    for k, name in enumerate(("x", "weight", "bias", "state")):
+        for i in range(g[name].size):
+            got = difference(lambda a, b, c, d: ref.conv_fwd(a, b, c, d, spans, act)[:2], (x, w, bias, state), k, i,
+                             (dy, df))
+            assert abs(got - g[name].reshape(-1)[i]) <= 1e-7 * (1 + abs(got)), (name, i)
+
+
+def test_conv_of_an_impulse_is_its_taps():
+    w = np.array([[0.5, -1.0, 2.0, 3.0]])
+    x = np.zeros((6, 1))
+    x[1] = 1
+    y, final, _ = ref.conv_fwd(x, w, None, np.zeros((1, 3, 1)), [(0, 6)], False)
+    assert np.array_equal(y[:, 0], [0, 3, 2, -1, 0.5, 0]) and np.array_equal(final[0], x[3:])
