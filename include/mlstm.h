@@ -534,6 +534,49 @@ mlstm_status ssm_conv_bwd(const void *x, long long x_stride, const float *weight
                           void *grad_state_init,
                           void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Selective state space scan.  Channel d belongs to group g = d / (D / G) and keeps
+ * N states; per row t
+ *   s_t  = softplus(dt_t + dt_bias), or dt_t + dt_bias with softplus = 0
+ *   h_t[n] = exp(s_t A[d][n]) h_{t-1}[n] + s_t x_t B_t[g][n]
+ *   o_t  = sum_n C_t[g][n] h_t[n] + Dskip[d] x_t
+ *   y_t  = o_t, or o_t z_t sigmoid(z_t) with z
+ * softplus(v) = log(1 + e^v), taken as v above 20.  The state, the step size and all
+ * sums are fp32.
+ *   x, dt, z, y_out [rows,D] dtype (z NULL = no gate)
+ *   A [D,N];  Dskip, dt_bias [D] or NULL (= 0)
+ *   Bm, Cm [rows,G,N] dtype: element (row, g, n) at row*stride + g*N + n
+ *   h_init [B,D,N] or NULL (= 0): the state that enters row 0
+ *   h_final [B,D,N] or NULL (not wanted): the state after the last row; may not be
+ *   h_init's buffer
+ *   D a multiple of G;  1 <= N <= 64
+ *   workspace: ssm_scan_fwd_workspace_bytes(...) bytes (may be 0), 16-byte aligned
+ * A sequence that fills too little of the chip is cut into pieces: their states are
+ * computed from zero first, then joined, and every piece runs from its true state.
+ */
+size_t ssm_scan_fwd_workspace_bytes(int B, int S, int D, int G, int N);
+mlstm_status ssm_scan_fwd(const void *x, long long x_stride, const void *dt, long long dt_stride,
+                          const float *A, const void *Bm, long long B_stride,
+                          const void *Cm, long long C_stride,
+                          const float *Dskip, const float *dt_bias,
+                          const void *z, long long z_stride,
+                          const int *seq_start, const float *h_init,
+                          int B, int S, int rows, int D, int G, int N, int softplus, mlstm_dtype dtype,
+                          void *y_out, long long y_stride, float *h_final,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One row of the scan for each of B sequences (x, dt, z, y_out [B,D]; Bm, Cm [B,G,N]);
+ * h [B,D,N] is updated in place.
+ */
+mlstm_status ssm_step(const void *x, long long x_stride, const void *dt, long long dt_stride,
+                      const float *A, const void *Bm, long long B_stride,
+                      const void *Cm, long long C_stride,
+                      const float *Dskip, const float *dt_bias,
+                      const void *z, long long z_stride,
+                      int B, int D, int G, int N, int softplus, mlstm_dtype dtype,
+                      float *h, void *y_out, long long y_stride, void *stream);
+
 /* Static description of a status code. */
 const char *mlstm_status_string(mlstm_status status);
 

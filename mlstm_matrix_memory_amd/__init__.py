@@ -23,6 +23,8 @@ Entry points (same names as include/mlstm.h):
   ssm_conv_fwd, ssm_conv_step, ssm_conv_bwd
                       short causal depthwise convolution with swish, for sequences and for
                       single rows, and its backward
+  ssm_scan_fwd, ssm_step
+                      selective state space scan for sequences and for single rows
   mlstm_fwd_workspace_bytes, mlstm_status_string, mlstm_error_detail
 """
 from .binding import (  # noqa: F401
@@ -60,4 +62,7 @@ from .binding import (  # noqa: F401
     ssm_conv_bwd_workspace_bytes,
     ssm_conv_fwd,
     ssm_conv_step,
+    ssm_scan_fwd,
+    ssm_scan_fwd_workspace_bytes,
+    ssm_step,
 )

@@ -105,6 +105,13 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     lib.ssm_conv_bwd.restype = i
     lib.ssm_conv_bwd.argtypes = [vp, ll, vp, vp, vp, vp, vp, ll, vp, i, i, i, i, i, i, i, vp, ll, vp, vp, vp, vp, sz,
                                  vp]
+    lib.ssm_scan_fwd_workspace_bytes.restype = sz
+    lib.ssm_scan_fwd_workspace_bytes.argtypes = [i, i, i, i, i]
+    lib.ssm_scan_fwd.restype = i
+    lib.ssm_scan_fwd.argtypes = [vp, ll, vp, ll, vp, vp, ll, vp, ll, vp, vp, vp, ll, vp, vp, i, i, i, i, i, i, i, i,
+                                 vp, ll, vp, vp, sz, vp]
+    lib.ssm_step.restype = i
+    lib.ssm_step.argtypes = [vp, ll, vp, ll, vp, vp, ll, vp, ll, vp, vp, vp, ll, i, i, i, i, i, i, vp, vp, ll, vp]
     lib.mlstm_status_string.restype = ctypes.c_char_p
     lib.mlstm_status_string.argtypes = [i]
     lib.mlstm_error_detail.restype = ctypes.c_char_p
@@ -883,3 +890,74 @@ def ssm_conv_bwd(x, weight, dy, bias=None, act: int = SSM_ACT_SWISH, state_init=
             grad_x.data_ptr(), _row_stride(grad_x, "grad_x"), grad_weight.data_ptr(), _ptr(grad_bias),
             _ptr(grad_state), ws, ws_bytes, _stream_handle(stream, dev))
     return grad_x, grad_weight, grad_bias, grad_state
+
+
+def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, batch, dev):
+    """Checks the scan's inputs; returns (its shared argument list, G, N)."""
+    import torch
+    width, N = A.shape if A.dim() == 2 else (None, None)
+    if N is None or B.dim() != x.dim() + 1:
+        raise ValueError("A must be 2-D [D, N], and B and C must have x's leading dimensions followed by [G, N]")
+    lead, G = tuple(x.shape[:-1]), B.shape[-2]
+    _check_rows(x, "x", (*lead, width), x.dtype, dev)
+    _check_rows(dt, "dt", (*lead, width), x.dtype, dev)
+    _check(A, "A", (width, N), torch.float32, dev)
+    for t, name in ((B, "B"), (C, "C")):
+        _check_rows(t, name, (*lead, G, N), x.dtype, dev)
+    for t, name in ((D, "D"), (dt_bias, "dt_bias")):
+        if t is not None:
+            _check(t, name, (width,), torch.float32, dev)
+    if z is not None:
+        _check_rows(z, "z", (*lead, width), x.dtype, dev)
+    args = [x.data_ptr(), _row_stride(x, "x"), dt.data_ptr(), _row_stride(dt, "dt"), A.data_ptr(),
+            B.data_ptr(), _row_stride(B, "B", 2), C.data_ptr(), _row_stride(C, "C", 2), _ptr(D), _ptr(dt_bias),
+            _ptr(z), 0 if z is None else _row_stride(z, "z")]
+    return args, width, G, N
+
+
+def ssm_scan_fwd_workspace_bytes(B: int, S: int, D: int, G: int, N: int) -> int:
+    return int(load_library().ssm_scan_fwd_workspace_bytes(B, S, D, G, N))
+
+
+def ssm_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True, h_init=None, seq_start=None,
+                 max_len=None, y_out=None, h_final=None, workspace=None, stream=None):
+    """Selective state space scan; returns (y, h_final).
+
+    x, dt, z [batch,S,D] (or packed [rows,D] with seq_start int32 [batch+1] and max_len)
+    and B, C [batch,S,G,N] in one dtype, float32 or bfloat16; A [D,N], D [D] and
+    dt_bias [D] float32; h_init and h_final [batch,D,N] float32 (None = zero).
+    """
+    import torch
+    dev, code = _gpu(x, "x"), _dtype_code(x)
+    batch, S, rows = _batch(x, seq_start, max_len, dev)
+    args, width, G, N = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, batch, dev)
+    if h_init is not None:
+        _check(h_init, "h_init", (batch, width, N), torch.float32, dev)
+    owned = []
+    y_out = _output(y_out, "y_out", x.shape, x.dtype, dev, owned)
+    h_final = _output(h_final, "h_final", (batch, width, N), torch.float32, dev, owned)
+    _check(h_final, "h_final", (batch, width, N), torch.float32, dev)
+    ws, ws_bytes = _workspace(workspace, ssm_scan_fwd_workspace_bytes(batch, S, width, G, N), dev, owned)
+    _keep_for_stream(stream, dev, owned)
+    _launch("ssm_scan_fwd", dev, *args, _ptr(seq_start), _ptr(h_init), batch, S, rows, width, G, N, int(softplus), code,
+            y_out.data_ptr(), _row_stride(y_out, "y_out"), h_final.data_ptr(), ws, ws_bytes,
+            _stream_handle(stream, dev))
+    return y_out, h_final
+
+
+def ssm_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None, softplus: bool = True, y_out=None, stream=None):
+    """One row of the scan per sequence: x, dt, z [batch,D], B, C [batch,G,N]; the state
+    h [batch,D,N] float32 is updated in place.  Returns y [batch,D]."""
+    import torch
+    dev, code = _gpu(x, "x"), _dtype_code(x)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [batch, D]")
+    batch = x.shape[0]
+    args, width, G, N = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, batch, dev)
+    _check(h, "h", (batch, width, N), torch.float32, dev)
+    owned = []
+    y_out = _output(y_out, "y_out", x.shape, x.dtype, dev, owned)
+    _keep_for_stream(stream, dev, owned)
+    _launch("ssm_step", dev, *args, batch, width, G, N, int(softplus), code, h.data_ptr(), y_out.data_ptr(),
+            _row_stride(y_out, "y_out"), _stream_handle(stream, dev))
+    return y_out

@@ -146,9 +146,51 @@ def test_conv_bwd_workspace(lib):
     assert b.ssm_conv_bwd_workspace_bytes(2, 0, 64, 4) == 0 and b.ssm_conv_bwd_workspace_bytes(2, 8, 64, 9) == 0
 
 
+SCAN = dict(x=P[0], xs=64, dtp=P[1], dts=64, A=P[2], Bm=P[3], bs=16, Cm=P[4], cs=16, skip=P[5], bias=P[6], z=P[7],
+            zs=64, start=None, h0=P[8], B=2, S=8, rows=16, D=64, G=1, N=16, softplus=1, dt=1)
+SCAN_BAD = [
+    (dict(D=63, G=2, xs=63, dts=63, zs=63), "D=63 is not a multiple of G=2"), (dict(G=0), "G=0"), (dict(N=0), "N=0"),
+    (dict(N=65, bs=65, cs=65), "N=65"), (dict(softplus=2), "softplus=2"), (dict(dtp=None), "dt is NULL"),
+    (dict(A=None), "A is NULL"), (dict(Bm=None), "Bm is NULL"), (dict(Cm=None), "Cm is NULL"), (dict(bs=15), "Bm_stride=15"),
+    (dict(zs=1), "z_stride=1"), (dict(A=P[2] + 2), "A is not 4-byte aligned"),
+]
+
+
+def _scan(lib, **kw):
+    a = dict(SCAN, y=P[9], ys=64, final=P[10], ws=P[11], n=1 << 30)
+    a.update(kw)
+    return lib.ssm_scan_fwd(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,words", BATCH_BAD + SCAN_BAD + [
+    (dict(y=None), "y_out is NULL"), (dict(y=P[1]), "y_out overlaps dt"), (dict(final=P[8]), "h_final overlaps h_init"),
+    (dict(y=P[7], ys=64), "y_out overlaps z")])
+def test_scan_refusals(lib, kw, words):
+    refused(_scan(lib, **kw), words)
+
+
+def test_scan_workspace(lib):
+    big = dict(B=1, S=65536, rows=65536)
+    need = b.ssm_scan_fwd_workspace_bytes(1, 65536, 64, 1, 16)
+    if need:
+        refused(_scan(lib, n=need - 1, **big), "needed", b.MLSTM_ERR_WORKSPACE)
+        refused(_scan(lib, ws=P[11] + 4, **big), "workspace is not 16-byte aligned")
+    for bad in ((0, 8, 64, 1, 16), (2, 0, 64, 1, 16), (2, 8, 64, 3, 16), (2, 8, 64, 1, 65)):
+        assert b.ssm_scan_fwd_workspace_bytes(*bad) == 0
+
+
+@pytest.mark.parametrize("kw,words", SCAN_BAD + [
+    (dict(B=0), "B=0"), (dict(h=None), "h is NULL"), (dict(y=P[10]), "overlaps"), (dict(h=P[2]), "h overlaps A")])
+def test_ssm_step_refusals(lib, kw, words):
+    a = {k: v for k, v in SCAN.items() if k not in ("start", "h0", "S", "rows")}
+    a.update(h=P[10], y=P[9], ys=64)
+    a.update(kw)
+    refused(lib.ssm_step(*a.values(), None), words)
+
+
 def test_block_operators_exported(lib):
     import mlstm_matrix_memory_amd as pkg
     for name in ("mlstm_rms_norm_fwd", "mlstm_rms_norm_quant", "mlstm_rms_norm_bwd",
                  "mlstm_rms_norm_bwd_workspace_bytes", "ssm_conv_fwd", "ssm_conv_step", "ssm_conv_bwd",
-                 "ssm_conv_bwd_workspace_bytes"):
+                 "ssm_conv_bwd_workspace_bytes", "ssm_scan_fwd", "ssm_step", "ssm_scan_fwd_workspace_bytes"):
         assert name in b.header_symbols() and hasattr(lib, name) and callable(getattr(pkg, name))

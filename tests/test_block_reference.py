@@ -63,3 +63,54 @@ def test_conv_of_an_impulse_is_its_taps():
     x[1] = 1
     y, final, _ = ref.conv_fwd(x, w, None, np.zeros((1, 3, 1)), [(0, 6)], False)
     assert np.array_equal(y[:, 0], [0, 3, 2, -1, 0.5, 0]) and np.array_equal(final[0], x[3:])
+
+
+def _scan_case(rng, gate, softplus):
+    start = [0, 3, 3, 4, 7]
+    D, G, N = 4, 2, 3
+    c = {"x": rng.standard_normal((7, D)), "dt": rng.standard_normal((7, D)) - (0 if softplus else -1.5),
+         "z": rng.standard_normal((7, D)) if gate else None, "A": -np.exp(rng.standard_normal((D, N))),
+         "B": rng.standard_normal((7, G, N)), "C": rng.standard_normal((7, G, N)), "D": rng.standard_normal(D),
+         "dt_bias": rng.standard_normal(D), "h": rng.standard_normal((4, D, N)), "spans": ref.sequences(4, 3, start),
+         "softplus": softplus}
+    return c
+
+
+@pytest.mark.parametrize("gate,softplus", [(True, 1), (False, 0)])
+def test_scan_gradients_are_differences(gate, softplus):
+    rng = np.random.default_rng(3 + softplus)
+    c = _scan_case(rng, gate, softplus)
+    dy, dh = rng.standard_normal((7, 4)), rng.standard_normal((4, 4, 3))
+    got = ref.scan(c, dy, dh)
+    names = [k for k in ("x", "dt", "z", "A", "B", "C", "D", "dt_bias", "h") if c[k] is not None]
+
+    def f(*args):
+        out = ref.scan(dict(c, **dict(zip(names, args))))
+        return out["y"][0], out["h_final"][0]
+
+    for k, name in enumerate(names):
+        grad, bound = got["grad_" + name]
+        assert np.all(bound >= 0)
+        for i in range(grad.size):
+            d = difference(f, [c[n] for n in names], k, i, (dy, dh))
+            assert abs(d - grad.reshape(-1)[i]) <= 2e-7 * (1 + abs(d)), (name, i)
+
+
+def test_scan_without_decay_is_a_running_sum():
+    rng = np.random.default_rng(8)
+    c = _scan_case(rng, False, 0)
+    c.update(A=np.zeros((4, 3)), D=None, dt_bias=None, dt=np.ones((7, 4)), C=np.ones((7, 2, 3)), B=np.ones((7, 2, 3)),
+             h=None)
+    y = ref.scan(c)["y"][0]
+    for lo, hi in c["spans"]:
+        assert np.allclose(y[lo:hi], 3 * np.cumsum(c["x"][lo:hi], 0), atol=1e-12)
+
+
+def test_scan_with_full_forgetting_keeps_one_row():
+    rng = np.random.default_rng(9)
+    c = _scan_case(rng, False, 0)
+    c.update(A=np.full((4, 3), -1e4), dt=np.full((7, 4), 1.0), dt_bias=None, h=None)
+    y = ref.scan(c)["y"][0]
+    for t in range(7):
+        bc = (c["B"][t] * c["C"][t]).sum(1).repeat(2)
+        assert np.allclose(y[t], c["x"][t] * (bc + c["D"]), atol=1e-12)
