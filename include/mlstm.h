@@ -577,6 +577,30 @@ mlstm_status ssm_step(const void *x, long long x_stride, const void *dt, long lo
                       int B, int D, int G, int N, int softplus, mlstm_dtype dtype,
                       float *h, void *y_out, long long y_stride, void *stream);
 
+/*
+ * Backward of ssm_scan_fwd, from its inputs and dy [rows,D] dtype.
+ *   dh_final [B,D,N] or NULL: gradient of h_final
+ *   grad_x, grad_dt, grad_z [rows,D] dtype (grad_z NULL if z is)
+ *   grad_B, grad_C [rows,G,N] dtype, laid out like Bm and Cm with their own strides
+ *   grad_A [D,N];  grad_Dskip, grad_dt_bias [D] (NULL if the parameter is)
+ *   grad_h_init [B,D,N], or NULL (not wanted)
+ *   workspace: ssm_scan_bwd_workspace_bytes(...) bytes, 16-byte aligned
+ */
+size_t ssm_scan_bwd_workspace_bytes(int B, int S, int rows, int D, int G, int N);
+mlstm_status ssm_scan_bwd(const void *x, long long x_stride, const void *dt, long long dt_stride,
+                          const float *A, const void *Bm, long long B_stride,
+                          const void *Cm, long long C_stride,
+                          const float *Dskip, const float *dt_bias,
+                          const void *z, long long z_stride,
+                          const int *seq_start, const float *h_init,
+                          const void *dy, long long dy_stride, const float *dh_final,
+                          int B, int S, int rows, int D, int G, int N, int softplus, mlstm_dtype dtype,
+                          void *grad_x, long long grad_x_stride, void *grad_dt, long long grad_dt_stride,
+                          void *grad_z, long long grad_z_stride,
+                          void *grad_B, long long grad_B_stride, void *grad_C, long long grad_C_stride,
+                          float *grad_A, float *grad_Dskip, float *grad_dt_bias, float *grad_h_init,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
 /* Static description of a status code. */
 const char *mlstm_status_string(mlstm_status status);
 

@@ -25,6 +25,7 @@ Entry points (same names as include/mlstm.h):
                       single rows, and its backward
   ssm_scan_fwd, ssm_step
                       selective state space scan for sequences and for single rows
+  ssm_scan_bwd        gradients of the selective scan with respect to all inputs
   mlstm_fwd_workspace_bytes, mlstm_status_string, mlstm_error_detail
 """
 from .binding import (  # noqa: F401
@@ -65,4 +66,6 @@ from .binding import (  # noqa: F401
     ssm_scan_fwd,
     ssm_scan_fwd_workspace_bytes,
     ssm_step,
+    ssm_scan_bwd,
+    ssm_scan_bwd_workspace_bytes,
 )

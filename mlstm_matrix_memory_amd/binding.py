@@ -112,6 +112,11 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
                                  vp, ll, vp, vp, sz, vp]
     lib.ssm_step.restype = i
     lib.ssm_step.argtypes = [vp, ll, vp, ll, vp, vp, ll, vp, ll, vp, vp, vp, ll, i, i, i, i, i, i, vp, vp, ll, vp]
+    lib.ssm_scan_bwd_workspace_bytes.restype = sz
+    lib.ssm_scan_bwd_workspace_bytes.argtypes = [i, i, i, i, i, i]
+    lib.ssm_scan_bwd.restype = i
+    lib.ssm_scan_bwd.argtypes = [vp, ll, vp, ll, vp, vp, ll, vp, ll, vp, vp, vp, ll, vp, vp, vp, ll, vp, i, i, i, i,
+                                 i, i, i, i, vp, ll, vp, ll, vp, ll, vp, ll, vp, ll, vp, vp, vp, vp, vp, sz, vp]
     lib.mlstm_status_string.restype = ctypes.c_char_p
     lib.mlstm_status_string.argtypes = [i]
     lib.mlstm_error_detail.restype = ctypes.c_char_p
@@ -961,3 +966,49 @@ def ssm_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None, softplus: bool = T
     _launch("ssm_step", dev, *args, batch, width, G, N, int(softplus), code, h.data_ptr(), y_out.data_ptr(),
             _row_stride(y_out, "y_out"), _stream_handle(stream, dev))
     return y_out
+
+
+def ssm_scan_bwd_workspace_bytes(B: int, S: int, rows: int, D: int, G: int, N: int) -> int:
+    return int(load_library().ssm_scan_bwd_workspace_bytes(B, S, rows, D, G, N))
+
+
+def ssm_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, softplus: bool = True, h_init=None, seq_start=None,
+                 max_len=None, dh_final=None, grad_x=None, grad_dt=None, grad_z=None, grad_B=None, grad_C=None,
+                 workspace=None, stream=None):
+    """Backward of ssm_scan_fwd; returns the gradients of (x, dt, A, B, C, D, z, dt_bias, h_init).
+
+    Inputs as for the forward, dy like x, dh_final like h_init.  Gradients of x, dt, z, B
+    and C have their dtype (given, they may be column ranges of wider tensors), the
+    others are float32; those of absent inputs are None.
+    """
+    import torch
+    dev, code = _gpu(x, "x"), _dtype_code(x)
+    batch, S, rows = _batch(x, seq_start, max_len, dev)
+    args, width, G, N = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, batch, dev)
+    _check_rows(dy, "dy", x.shape, x.dtype, dev)
+    for t, name in ((h_init, "h_init"), (dh_final, "dh_final")):
+        if t is not None:
+            _check(t, name, (batch, width, N), torch.float32, dev)
+    owned = []
+    grad_x = _output(grad_x, "grad_x", x.shape, x.dtype, dev, owned)
+    grad_dt = _output(grad_dt, "grad_dt", x.shape, x.dtype, dev, owned)
+    if z is not None:
+        grad_z = _output(grad_z, "grad_z", x.shape, x.dtype, dev, owned)
+    elif grad_z is not None:
+        raise ValueError("grad_z is given without z")
+    grad_B = _output(grad_B, "grad_B", B.shape, x.dtype, dev, owned)
+    grad_C = _output(grad_C, "grad_C", C.shape, x.dtype, dev, owned)
+    grad_A = torch.empty((width, N), dtype=torch.float32, device=dev)
+    grad_D = None if D is None else torch.empty((width,), dtype=torch.float32, device=dev)
+    grad_bias = None if dt_bias is None else torch.empty((width,), dtype=torch.float32, device=dev)
+    grad_h = None if h_init is None else torch.empty((batch, width, N), dtype=torch.float32, device=dev)
+    owned += [grad_A, grad_D, grad_bias, grad_h]
+    ws, ws_bytes = _workspace(workspace, ssm_scan_bwd_workspace_bytes(batch, S, rows, width, G, N), dev, owned)
+    _keep_for_stream(stream, dev, owned)
+    _launch("ssm_scan_bwd", dev, *args, _ptr(seq_start), _ptr(h_init), dy.data_ptr(), _row_stride(dy, "dy"),
+            _ptr(dh_final), batch, S, rows, width, G, N, int(softplus), code,
+            grad_x.data_ptr(), _row_stride(grad_x, "grad_x"), grad_dt.data_ptr(), _row_stride(grad_dt, "grad_dt"),
+            _ptr(grad_z), 0 if grad_z is None else _row_stride(grad_z, "grad_z"),
+            grad_B.data_ptr(), _row_stride(grad_B, "grad_B", 2), grad_C.data_ptr(), _row_stride(grad_C, "grad_C", 2),
+            grad_A.data_ptr(), _ptr(grad_D), _ptr(grad_bias), _ptr(grad_h), ws, ws_bytes, _stream_handle(stream, dev))
+    return grad_x, grad_dt, grad_A, grad_B, grad_C, grad_D, grad_z, grad_bias, grad_h

@@ -103,7 +103,8 @@ inline mlstm_status batch(int B, int S, int rows, int D, const int* seq_start) {
     if (!seq_start && (long long)B * S != rows)
         return fail(MLSTM_ERR_INVALID_ARG, "rows=%d is not B*S=%lld", rows, (long long)B * S);
     if (S > rows) return fail(MLSTM_ERR_INVALID_ARG, "S=%d exceeds rows=%d", S, rows);
-    if ((long long)rows * D > (1LL << 40)) return fail(MLSTM_ERR_UNSUPPORTED, "tensor too large");
+    // row indexes, also rounded up to tiles of rows, are 32-bit in the kernels
+    if (rows > (1 << 30) || (long long)rows * D > (1LL << 40)) return fail(MLSTM_ERR_UNSUPPORTED, "tensor too large");
     if (reinterpret_cast<uintptr_t>(seq_start) % 4)
         return fail(MLSTM_ERR_INVALID_ARG, "seq_start is not 4-byte aligned");
     return MLSTM_OK;

@@ -113,4 +113,57 @@ mlstm_status ssm_step(const void* x, long long x_stride, const void* dt, long lo
     return launched(mlstm::launch_ssm_step(a));
 }
 
+size_t ssm_scan_bwd_workspace_bytes(int B, int S, int rows, int D, int G, int N) {
+    if (!sizes_ok(B, S, D, G, N) || rows < 1 || rows > (1 << 30)) return 0;
+    return mlstm::scan_bwd_workspace_bytes(B, S, rows, D, G, N);
+}
+
+mlstm_status ssm_scan_bwd(const void* x, long long x_stride, const void* dt, long long dt_stride,
+                          const float* A, const void* Bm, long long B_stride, const void* Cm, long long C_stride,
+                          const float* Dskip, const float* dt_bias, const void* z, long long z_stride,
+                          const int* seq_start, const float* h_init,
+                          const void* dy, long long dy_stride, const float* dh_final,
+                          int B, int S, int rows, int D, int G, int N, int softplus, mlstm_dtype dtype,
+                          void* grad_x, long long grad_x_stride, void* grad_dt, long long grad_dt_stride,
+                          void* grad_z, long long grad_z_stride,
+                          void* grad_B, long long grad_B_stride, void* grad_C, long long grad_C_stride,
+                          float* grad_A, float* grad_Dskip, float* grad_dt_bias, float* grad_h_init,
+                          void* ws, size_t workspace_bytes, void* stream) {
+    const Inputs in = {x, x_stride, dt, dt_stride, A, Bm, B_stride, Cm, C_stride, Dskip, dt_bias, z, z_stride,
+                       seq_start, h_init, B, S, rows, D, G, N, softplus, dtype, stream};
+    constexpr int COUNT = INPUTS + 12;
+    Region r[COUNT];
+    MLSTM_TRY(check_inputs(in, r));
+    const size_t need = mlstm::scan_bwd_workspace_bytes(B, S, rows, D, G, N);
+    MLSTM_TRY(workspace(ws, workspace_bytes, need, 16));
+    if (!z && grad_z) return fail(MLSTM_ERR_INVALID_ARG, "grad_z is given without z");
+    if (!Dskip && grad_Dskip) return fail(MLSTM_ERR_INVALID_ARG, "grad_Dskip is given without Dskip");
+    if (!dt_bias && grad_dt_bias) return fail(MLSTM_ERR_INVALID_ARG, "grad_dt_bias is given without dt_bias");
+    const size_t el = elem(dtype), w = D, bc = (size_t)G * N, st = (size_t)B * D * N;
+    const Region more[COUNT - INPUTS] = {
+        strided(dy, rows, w, dy_stride, el, "dy"),
+        dense(dh_final, st, 4, "dh_final", false, true),
+        strided(grad_x, rows, w, grad_x_stride, el, "grad_x", true),
+        strided(grad_dt, rows, w, grad_dt_stride, el, "grad_dt", true),
+        strided(grad_z, rows, w, z ? grad_z_stride : (long long)D, el, "grad_z", true, !z),
+        strided(grad_B, rows, bc, grad_B_stride, el, "grad_B", true),
+        strided(grad_C, rows, bc, grad_C_stride, el, "grad_C", true),
+        dense(grad_A, w * N, 4, "grad_A", true),
+        dense(grad_Dskip, w, 4, "grad_Dskip", true, !Dskip),
+        dense(grad_dt_bias, w, 4, "grad_dt_bias", true, !dt_bias),
+        dense(grad_h_init, st, 4, "grad_h_init", true, true),
+        dense(ws, need, 1, "workspace", true),
+    };
+    for (int k = 0; k < COUNT - INPUTS; ++k) r[INPUTS + k] = more[k];
+    MLSTM_TRY(regions(r, COUNT));
+    MLSTM_TRY(disjoint(r, COUNT));
+    mlstm::ScanArgs a = make(in);
+    a.dy = dy; a.dy_stride = dy_stride; a.dh_final = dh_final;
+    a.grad_x = grad_x; a.grad_x_stride = grad_x_stride; a.grad_dt = grad_dt; a.grad_dt_stride = grad_dt_stride;
+    a.grad_z = grad_z; a.grad_z_stride = grad_z_stride; a.grad_B = grad_B; a.grad_B_stride = grad_B_stride;
+    a.grad_C = grad_C; a.grad_C_stride = grad_C_stride; a.grad_A = grad_A; a.grad_Dskip = grad_Dskip;
+    a.grad_dt_bias = grad_dt_bias; a.grad_h = grad_h_init; a.ws = (float*)ws;
+    return launched(mlstm::launch_scan_bwd(a));
+}
+
 }  // extern "C"

@@ -10,6 +10,9 @@ from mlstm_matrix_memory_amd import inputs
 # half a step of each storage type, relative to the value
 HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
 U = 2.0 ** -24
+# the smallest normal fp32 number: the hardware exponential gives zero below it, and results
+# below it may be flushed, so each such result is off by at most this much
+TINY = 2.0 ** -126
 
 
 def stored(a, dtype):
@@ -175,7 +178,7 @@ def scan(c, dy=None, dh_final=None, joins=False):
             a, ub = a_all[t], u[t][:, None] * _wide(Bm[t], D)
             E = a * E + np.abs(a * h) * (ea[t] + U) + eu[t][:, None] * np.abs(_wide(Bm[t], D)) + 2 * U * np.abs(ub)
             h = a * h + ub
-            E = E + U * np.abs(h)
+            E = E + U * np.abs(h) + TINY * (1 + np.abs(before[t]))
             most = np.maximum(most, np.abs(h))
             if joins:
                 E = np.maximum(E, 0) + (0.4 * U * most if t > lo else 0)
@@ -212,12 +215,13 @@ def scan(c, dy=None, dh_final=None, joins=False):
             Ct, Bt, a = _wide(Cm[t], D), _wide(Bm[t], D), a_all[t]
             q = ds[t][:, None] * Ct
             gr = nxt + q
-            E = En + eds[t][:, None] * np.abs(Ct) + U * np.abs(q) + U * np.abs(gr)
+            E = En + eds[t][:, None] * np.abs(Ct) + U * np.abs(q) + U * np.abs(gr) + TINY
             most = np.maximum(most, np.abs(gr))
             if joins:
                 E = E + 0.4 * U * most
             w = gr * a * before[t]
-            ew = (E * np.abs(a * before[t]) + np.abs(gr * a) * Ebefore[t] + np.abs(w) * (ea[t] + 3 * U))
+            ew = (E * np.abs(a * before[t]) + np.abs(gr * a) * Ebefore[t] + np.abs(w) * (ea[t] + 3 * U)
+                  + TINY * (1 + np.abs(gr) + np.abs(gr * before[t])))
             du = (gr * Bt).sum(1)
             edu = (E * np.abs(Bt) + np.abs(gr * Bt) * (N + 3) * U).sum(1)
             das = (w * A).sum(1)
@@ -237,8 +241,12 @@ def scan(c, dy=None, dh_final=None, joins=False):
             for k, val, er in (("B", dB, eB), ("C", dC, eC)):
                 g[k][t], e[k][t] = val.reshape(G, D // G, N).sum(1), er.reshape(G, D // G, N).sum(1)
             nxt = gr * a
-            En = E * a + np.abs(nxt) * (ea[t] + U)
+            En = E * a + np.abs(nxt) * (ea[t] + U) + TINY * (1 + np.abs(gr))
         g["h"][b], e["h"][b] = nxt, En
+    inside = np.zeros((rows, 1))
+    for lo, hi in c["spans"]:
+        inside[lo:hi] = 1
+    ds, eds = ds * inside, eds * inside
     g["D"], e["D"] = (ds * x).sum(0), ((eds + (rows + 3) * U * np.abs(ds)) * np.abs(x)).sum(0)
     g["dt_bias"], e["dt_bias"] = g["dt"].sum(0), (e["dt"] + (rows + 3) * U * np.abs(g["dt"])).sum(0)
     out.update({f"grad_{k}": (g[k], e[k]) for k in g})

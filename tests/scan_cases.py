@@ -2,7 +2,7 @@
 import numpy as np
 
 import block_reference as ref
-from block_reference import HALF, assert_within
+from block_reference import HALF, TINY, assert_within
 from gpu_helpers import to_gpu, to_np
 
 PACKED = [0, 5, 5, 6, 39, 41, 44, 177]            # lengths 5, 0, 1, 33, 2, 3, 133
@@ -59,7 +59,7 @@ def compare(c, name, tensor, want, dtype):
     Returns the rows outside of them."""
     value, bound = want
     got = to_np(tensor).reshape(value.shape)
-    e = bound + HALF[dtype] * (np.abs(value) + bound)
+    e = bound + HALF[dtype] * (np.abs(value) + bound) + TINY
     if len(value) != len(c["x"]) or name in ("h_final", "grad_h", "grad_A", "grad_D", "grad_dt_bias"):
         assert_within(name, got, value, e)
         return None

@@ -188,9 +188,40 @@ def test_ssm_step_refusals(lib, kw, words):
     refused(lib.ssm_step(*a.values(), None), words)
 
 
+def _scan_bwd(lib, **kw):
+    a = dict(SCAN, dy=P[9], ds=64, dh=P[10], gx=P[11], gxs=64, gdt=P[12], gdts=64, gz=P[13], gzs=64, gB=P[14], gBs=16,
+             gC=P[15], gCs=16, gA=P[16], gD=P[17], gb=P[18], gh=P[19], ws=P[20], n=1 << 30)
+    a.update(kw)
+    order = ["x", "xs", "dtp", "dts", "A", "Bm", "bs", "Cm", "cs", "skip", "bias", "z", "zs", "start", "h0", "dy", "ds", "dh",
+             "B", "S", "rows", "D", "G", "N", "softplus", "dt"]
+    rest = [k for k in a if k not in order]
+    return lib.ssm_scan_bwd(*(a[k] for k in order + rest), None)
+
+
+@pytest.mark.parametrize("kw,words", [(dict(k, start=P[21]) if "start" in k and k["start"] == P[20] else k, w)
+                                      for k, w in BATCH_BAD] + SCAN_BAD + [
+    (dict(dy=None), "dy is NULL"), (dict(gx=None), "grad_x is NULL"), (dict(gz=None), "grad_z is NULL"),
+    (dict(gD=None), "grad_Dskip is NULL"), (dict(gb=None), "grad_dt_bias is NULL"), (dict(gA=None), "grad_A is NULL"),
+    (dict(z=None), "grad_z is given without z"), (dict(skip=None), "grad_Dskip is given without Dskip"),
+    (dict(bias=None), "grad_dt_bias is given without dt_bias"), (dict(gh=P[10]), "overlaps"),
+    (dict(gB=P[15]), "overlaps"), (dict(gx=P[9]), "overlaps"), (dict(gCs=15), "grad_C_stride=15"),
+])
+def test_scan_bwd_refusals(lib, kw, words):
+    refused(_scan_bwd(lib, **kw), words)
+
+
+def test_scan_bwd_workspace(lib):
+    need = b.ssm_scan_bwd_workspace_bytes(2, 8, 16, 64, 1, 16)
+    assert need > 0
+    refused(_scan_bwd(lib, n=need - 1), "needed", b.MLSTM_ERR_WORKSPACE)
+    refused(_scan_bwd(lib, ws=P[20] + 4), "workspace is not 16-byte aligned")
+    assert b.ssm_scan_bwd_workspace_bytes(2, 8, 0, 64, 1, 16) == 0
+
+
 def test_block_operators_exported(lib):
     import mlstm_matrix_memory_amd as pkg
     for name in ("mlstm_rms_norm_fwd", "mlstm_rms_norm_quant", "mlstm_rms_norm_bwd",
                  "mlstm_rms_norm_bwd_workspace_bytes", "ssm_conv_fwd", "ssm_conv_step", "ssm_conv_bwd",
-                 "ssm_conv_bwd_workspace_bytes", "ssm_scan_fwd", "ssm_step", "ssm_scan_fwd_workspace_bytes"):
+                 "ssm_conv_bwd_workspace_bytes", "ssm_scan_fwd", "ssm_step", "ssm_scan_fwd_workspace_bytes",
+                 "ssm_scan_bwd", "ssm_scan_bwd_workspace_bytes"):
         assert name in b.header_symbols() and hasattr(lib, name) and callable(getattr(pkg, name))
