@@ -554,7 +554,7 @@ mlstm_status ssm_conv_bwd(const void *x, long long x_stride, const float *weight
  * A sequence that fills too little of the chip is cut into pieces: their states are
  * computed from zero first, then joined, and every piece runs from its true state.
  */
-size_t ssm_scan_fwd_workspace_bytes(int B, int S, int D, int G, int N);
+size_t ssm_scan_fwd_workspace_bytes(int B, int S, int rows, int D, int G, int N);
 mlstm_status ssm_scan_fwd(const void *x, long long x_stride, const void *dt, long long dt_stride,
                           const float *A, const void *Bm, long long B_stride,
                           const void *Cm, long long C_stride,

@@ -106,7 +106,7 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     lib.ssm_conv_bwd.argtypes = [vp, ll, vp, vp, vp, vp, vp, ll, vp, i, i, i, i, i, i, i, vp, ll, vp, vp, vp, vp, sz,
                                  vp]
     lib.ssm_scan_fwd_workspace_bytes.restype = sz
-    lib.ssm_scan_fwd_workspace_bytes.argtypes = [i, i, i, i, i]
+    lib.ssm_scan_fwd_workspace_bytes.argtypes = [i, i, i, i, i, i]
     lib.ssm_scan_fwd.restype = i
     lib.ssm_scan_fwd.argtypes = [vp, ll, vp, ll, vp, vp, ll, vp, ll, vp, vp, vp, ll, vp, vp, i, i, i, i, i, i, i, i,
                                  vp, ll, vp, vp, sz, vp]
@@ -920,8 +920,8 @@ def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, batch, dev):
     return args, width, G, N
 
 
-def ssm_scan_fwd_workspace_bytes(B: int, S: int, D: int, G: int, N: int) -> int:
-    return int(load_library().ssm_scan_fwd_workspace_bytes(B, S, D, G, N))
+def ssm_scan_fwd_workspace_bytes(B: int, S: int, rows: int, D: int, G: int, N: int) -> int:
+    return int(load_library().ssm_scan_fwd_workspace_bytes(B, S, rows, D, G, N))
 
 
 def ssm_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True, h_init=None, seq_start=None,
@@ -942,7 +942,7 @@ def ssm_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = 
     y_out = _output(y_out, "y_out", x.shape, x.dtype, dev, owned)
     h_final = _output(h_final, "h_final", (batch, width, N), torch.float32, dev, owned)
     _check(h_final, "h_final", (batch, width, N), torch.float32, dev)
-    ws, ws_bytes = _workspace(workspace, ssm_scan_fwd_workspace_bytes(batch, S, width, G, N), dev, owned)
+    ws, ws_bytes = _workspace(workspace, ssm_scan_fwd_workspace_bytes(batch, S, rows, width, G, N), dev, owned)
     _keep_for_stream(stream, dev, owned)
     _launch("ssm_scan_fwd", dev, *args, _ptr(seq_start), _ptr(h_init), batch, S, rows, width, G, N, int(softplus), code,
             y_out.data_ptr(), _row_stride(y_out, "y_out"), h_final.data_ptr(), ws, ws_bytes,

@@ -95,7 +95,7 @@ inline mlstm_status workspace(const void* ws, size_t given, size_t need, size_t 
 }
 
 // sizes of a batch of sequences over rows of D channels
-constexpr int MAX_SEQUENCES = 65535;
+constexpr int MAX_SEQUENCES = 65535, MAX_ROWS = 1 << 30;
 inline mlstm_status batch(int B, int S, int rows, int D, const int* seq_start) {
     if (B < 1 || S < 1 || rows < 1 || D < 1)
         return fail(MLSTM_ERR_INVALID_ARG, "B=%d, S=%d, rows=%d, D=%d must all be >= 1", B, S, rows, D);
@@ -104,7 +104,7 @@ inline mlstm_status batch(int B, int S, int rows, int D, const int* seq_start) {
         return fail(MLSTM_ERR_INVALID_ARG, "rows=%d is not B*S=%lld", rows, (long long)B * S);
     if (S > rows) return fail(MLSTM_ERR_INVALID_ARG, "S=%d exceeds rows=%d", S, rows);
     // row indexes, also rounded up to tiles of rows, are 32-bit in the kernels
-    if (rows > (1 << 30) || (long long)rows * D > (1LL << 40)) return fail(MLSTM_ERR_UNSUPPORTED, "tensor too large");
+    if (rows > MAX_ROWS || (long long)rows * D > (1LL << 40)) return fail(MLSTM_ERR_UNSUPPORTED, "tensor too large");
     if (reinterpret_cast<uintptr_t>(seq_start) % 4)
         return fail(MLSTM_ERR_INVALID_ARG, "seq_start is not 4-byte aligned");
     return MLSTM_OK;

@@ -61,6 +61,49 @@ __device__ __forceinline__ void store_row8(T* p, const Raw8<T>& r, int n) {
     }
 }
 
+// four consecutive elements, likewise
+typedef __bf16 bf16x4_u __attribute__((ext_vector_type(4), aligned(2)));
+template <typename T> struct Raw4;
+template <> struct Raw4<bf16> {
+    bf16x4 v;
+    __device__ __forceinline__ float get(int e) const { return (float)v[e]; }
+    __device__ __forceinline__ void set(int e, float x) { v[e] = (bf16)x; }
+    __device__ __forceinline__ void load(const bf16* p) { v = *reinterpret_cast<const bf16x4_u*>(p); }
+    __device__ __forceinline__ void store(bf16* p) const { *reinterpret_cast<bf16x4_u*>(p) = v; }
+    __device__ __forceinline__ void zero() { v = bf16x4{0, 0, 0, 0}; }
+};
+template <> struct Raw4<float> {
+    f32x4 v;
+    __device__ __forceinline__ float get(int e) const { return v[e]; }
+    __device__ __forceinline__ void set(int e, float x) { v[e] = x; }
+    __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const f32x4_u*>(p); }
+    __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<f32x4_u*>(p) = v; }
+    __device__ __forceinline__ void zero() { v = f32x4{0, 0, 0, 0}; }
+};
+template <typename T>
+__device__ __forceinline__ Raw4<T> load_row4(const T* p, int n) {
+    Raw4<T> r;
+    if (n >= 4) {
+        r.load(p);
+    } else {
+        r.zero();
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < n) r.set(e, to_f32(p[e]));
+    }
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void store_row4(T* p, const Raw4<T>& r, int n) {
+    if (n >= 4) {
+        r.store(p);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < n) p[e] = from_f32<T>(r.get(e));
+    }
+}
+
 // ---- elementwise functions on the hardware exp, log and reciprocal -----------
 // (each within about 1 ulp)
 constexpr float LOG2E = 1.4426950408889634f;
@@ -79,7 +122,9 @@ __device__ __forceinline__ float softplus_hw(float v) {
     const float e = __builtin_amdgcn_exp2f(LOG2E * v);
     const float w = 1.0f + e;
     const float l = __builtin_amdgcn_logf(w) * LN2 * e * __builtin_amdgcn_rcpf(w - 1.0f);
-    return v > 20.0f ? v : (w == 1.0f ? e : l);
+    // selects, not branches: a wave's elements then run through the pipeline together
+    const float r = __builtin_unpredictable(w == 1.0f) ? e : l;
+    return __builtin_unpredictable(v > 20.0f) ? v : r;
 }
 
 // ---- rows of a sequence --------------------------------------------------------
@@ -92,6 +137,35 @@ __device__ __forceinline__ RowRange sequence_rows(const int* seq_start, int b, i
     const int lo = min(max(seq_start[b], 0), rows);
     const int hi = min(max(seq_start[b + 1], lo), rows);
     return RowRange{lo, min(hi - lo, S)};
+}
+
+// A batch cut into pieces of `length` rows, numbered through all sequences: `per`
+// pieces for each of equal length, or, packed, sequence b's pieces from number
+// lo / length + b on, which leaves room for its last, shorter one (no two sequences
+// share a number, and count() bounds them all by the rows that there are, however
+// unequal the sequences).
+struct Pieces {
+    const int* seq_start;
+    int B, S, rows, length, per;
+    struct At { int b, c; };             // the c-th piece of sequence b
+    __host__ __device__ int count() const { return seq_start ? rows / length + B : B * per; }
+    __device__ __forceinline__ int first(int b, const RowRange& sq) const {
+        return seq_start ? sq.lo / length + b : b * per;
+    }
+    __device__ __forceinline__ At at(int number) const {
+        if (!seq_start) return At{number / per, number % per};
+        int b = 0, end = B;              // the last sequence whose first number is not above this one
+        while (end - b > 1) {
+            const int mid = (b + end) >> 1;
+            if (min(max(seq_start[mid], 0), rows) / length + mid <= number) b = mid;
+            else end = mid;
+        }
+        return At{b, number - (min(max(seq_start[b], 0), rows) / length + b)};
+    }
+    __device__ __forceinline__ RowRange sequence(int b) const { return sequence_rows(seq_start, b, S, rows); }
+};
+inline Pieces make_pieces(const int* seq_start, int B, int S, int rows, int length) {
+    return Pieces{seq_start, B, S, rows, length, (S + length - 1) / length};
 }
 
 // ---- launchers -------------------------------------------------------------------
@@ -167,7 +241,7 @@ struct ScanArgs {
     float* grad_h;                                   // or null
 };
 constexpr int SCAN_MAX_N = 64;
-size_t scan_fwd_workspace_bytes(int B, int S, int D, int G, int N);
+size_t scan_fwd_workspace_bytes(int B, int S, int rows, int D, int G, int N);
 hipError_t launch_scan_fwd(const ScanArgs& a);
 hipError_t launch_ssm_step(const ScanArgs& a);
 size_t scan_bwd_workspace_bytes(int B, int S, int rows, int D, int G, int N);

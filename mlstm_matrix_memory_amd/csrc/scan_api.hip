@@ -7,13 +7,13 @@ namespace {
 using namespace mlstm::checks;
 using mlstm::fail;
 
-mlstm_status check_scan(int B, int S, int D, int G, int N) {
+mlstm_status check_scan(int B, int rows, int D, int G, int N) {
     if (G < 1 || D % G) return fail(MLSTM_ERR_INVALID_ARG, "D=%d is not a multiple of G=%d", D, G);
     if (N < 1 || N > mlstm::SCAN_MAX_N)
         return fail(MLSTM_ERR_INVALID_ARG, "N=%d must lie in [1, %d]", N, mlstm::SCAN_MAX_N);
-    // workgroups: tiles of 64 channels times sequences times pieces of a sequence
+    // workgroups: tiles of 64 channels times pieces, of which there are at most rows / 16 + B
     const long long tiles = (long long)G * ((D / G + 63) / 64);
-    if (tiles * B * ((S + 31) / 32) > 0x7fffffffLL) return fail(MLSTM_ERR_UNSUPPORTED, "batch too large");
+    if (tiles * (rows / 16 + B) > 0x7fffffffLL) return fail(MLSTM_ERR_UNSUPPORTED, "batch too large");
     return MLSTM_OK;
 }
 
@@ -28,7 +28,7 @@ constexpr int INPUTS = 10;
 
 mlstm_status check_inputs(const Inputs& i, Region* r) {
     MLSTM_TRY(batch(i.B, i.S, i.rows, i.D, i.seq_start));
-    MLSTM_TRY(check_scan(i.B, i.S, i.D, i.G, i.N));
+    MLSTM_TRY(check_scan(i.B, i.rows, i.D, i.G, i.N));
     if (i.softplus != 0 && i.softplus != 1)
         return fail(MLSTM_ERR_INVALID_ARG, "softplus=%d is neither 0 nor 1", i.softplus);
     MLSTM_TRY(dtype(i.dtype, "dtype"));
@@ -60,16 +60,17 @@ mlstm::ScanArgs make(const Inputs& i) {
     return a;
 }
 
-bool sizes_ok(int B, int S, int D, int G, int N) {
-    return B >= 1 && S >= 1 && D >= 1 && B <= MAX_SEQUENCES && check_scan(B, S, D, G, N) == MLSTM_OK;
+bool sizes_ok(int B, int S, int rows, int D, int G, int N) {
+    return B >= 1 && S >= 1 && D >= 1 && B <= MAX_SEQUENCES && rows >= 1 && rows <= MAX_ROWS && S <= rows &&
+           check_scan(B, rows, D, G, N) == MLSTM_OK;
 }
 
 }  // namespace
 
 extern "C" {
 
-size_t ssm_scan_fwd_workspace_bytes(int B, int S, int D, int G, int N) {
-    return sizes_ok(B, S, D, G, N) ? mlstm::scan_fwd_workspace_bytes(B, S, D, G, N) : 0;
+size_t ssm_scan_fwd_workspace_bytes(int B, int S, int rows, int D, int G, int N) {
+    return sizes_ok(B, S, rows, D, G, N) ? mlstm::scan_fwd_workspace_bytes(B, S, rows, D, G, N) : 0;
 }
 
 mlstm_status ssm_scan_fwd(const void* x, long long x_stride, const void* dt, long long dt_stride,
@@ -83,7 +84,7 @@ mlstm_status ssm_scan_fwd(const void* x, long long x_stride, const void* dt, lon
                        seq_start, h_init, B, S, rows, D, G, N, softplus, dtype, stream};
     Region r[INPUTS + 3];
     MLSTM_TRY(check_inputs(in, r));
-    const size_t need = mlstm::scan_fwd_workspace_bytes(B, S, D, G, N);
+    const size_t need = mlstm::scan_fwd_workspace_bytes(B, S, rows, D, G, N);
     MLSTM_TRY(workspace(ws, workspace_bytes, need, 16));
     r[INPUTS] = strided(y_out, rows, D, y_stride, elem(dtype), "y_out", true);
     r[INPUTS + 1] = dense(h_final, (size_t)B * D * N, 4, "h_final", true, true);
@@ -114,7 +115,7 @@ mlstm_status ssm_step(const void* x, long long x_stride, const void* dt, long lo
 }
 
 size_t ssm_scan_bwd_workspace_bytes(int B, int S, int rows, int D, int G, int N) {
-    if (!sizes_ok(B, S, D, G, N) || rows < 1 || rows > (1 << 30)) return 0;
+    if (!sizes_ok(B, S, rows, D, G, N)) return 0;
     return mlstm::scan_bwd_workspace_bytes(B, S, rows, D, G, N);
 }
 

@@ -31,38 +31,6 @@ namespace {
 
 constexpr int BWD_ROWS = 16;
 
-// four consecutive elements of a row, of which the first n are in it
-template <typename T> struct Raw4 { float v[4]; };
-template <typename T>
-__device__ __forceinline__ Raw4<T> load_row4(const T* p, int n) {
-    typedef T v4 __attribute__((ext_vector_type(4), aligned(sizeof(T))));
-    Raw4<T> r = {{0, 0, 0, 0}};
-    if (n >= 4) {
-        const v4 x = *reinterpret_cast<const v4*>(p);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) r.v[e] = (float)x[e];
-    } else {
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-            if (e < n) r.v[e] = to_f32(p[e]);
-    }
-    return r;
-}
-template <typename T>
-__device__ __forceinline__ void store_row4(T* p, const float* r, int n) {
-    typedef T v4 __attribute__((ext_vector_type(4), aligned(sizeof(T))));
-    if (n >= 4) {
-        v4 x;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = (T)r[e];
-        *reinterpret_cast<v4*>(p) = x;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-            if (e < n) p[e] = from_f32<T>(r[e]);
-    }
-}
-
 struct BwdParams {
     const void* x; const void* dt; const void* Bm; const void* Cm; const void* z; const void* dy;
     long long x_stride, dt_stride, B_stride, C_stride, z_stride, dy_stride;
@@ -104,7 +72,8 @@ struct Work {
     bool own, live;
     const T *xp, *dtp, *zp, *dyp, *bp, *cp;
     float bias[4];
-    Raw4<T> x[PASS], v[PASS], z[PASS], dy[PASS];       // the staged tile's: v = dt + bias
+    Raw4<T> x[PASS], z[PASS], dy[PASS];                // the staged tile's
+    float v[PASS][4];                                  // and its dt + bias
     Raw4<T> xn[PASS], vn[PASS], zn[PASS], dyn[PASS];   // the next tile's
     T bn[BCN], cn[BCN];
 
@@ -177,12 +146,12 @@ struct Work {
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                v[i].v[e] = vn[i].v[e] + bias[e];
-                const float s = row ? (p.softplus ? softplus_hw(v[i].v[e]) : v[i].v[e]) : 0.0f;
-                l.su[r][c4 + e] = float2{s, s * x[i].v[e]};
+                v[i][e] = vn[i].get(e) + bias[e];
+                const float s = row ? (p.softplus ? softplus_hw(v[i][e]) : v[i][e]) : 0.0f;
+                l.su[r][c4 + e] = float2{s, s * x[i].get(e)};
                 if (GRAD) {
-                    const float zv = z[i].v[e];
-                    l.ds[r][c4 + e] = p.z ? dy[i].v[e] * zv * sigmoid_hw(zv) : dy[i].v[e];
+                    const float zv = z[i].get(e);
+                    l.ds[r][c4 + e] = p.z ? dy[i].get(e) * zv * sigmoid_hw(zv) : dy[i].get(e);
                 }
             }
         }
@@ -388,7 +357,7 @@ __global__ __launch_bounds__(64 * NW) void scan_bwd_kernel(const BwdParams p)
         for (int i = 0; i < PASS; ++i) {
             const int r = w.r0 + (NT / 16) * i, t = t0 + r;
             const int n = t < w.t_end ? w.ch.count - w.c4 : 0;
-            float dx[4], ddt[4], dz[4];
+            Raw4<T> dx, ddt, dz;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float o = 0.0f, du = 0.0f, aw = 0.0f;
@@ -398,17 +367,18 @@ __global__ __launch_bounds__(64 * NW) void scan_bwd_kernel(const BwdParams p)
                     du += part[k][1][r][w.c4 + e];
                     aw += part[k][2][r][w.c4 + e];
                 }
-                const float s = lds.su[r][w.c4 + e].x, ds = lds.ds[r][w.c4 + e], x = w.x[i].v[e];
-                dx[e] = fmaf(s, du, skip[e] * ds);
-                ddt[e] = fmaf(aw, LN2, x * du);        // a2 carries log2(e)
-                if (p.softplus) ddt[e] *= sigmoid_hw(w.v[i].v[e]);
+                const float s = lds.su[r][w.c4 + e].x, ds = lds.ds[r][w.c4 + e], x = w.x[i].get(e);
+                dx.set(e, fmaf(s, du, skip[e] * ds));
+                float g = fmaf(aw, LN2, x * du);       // a2 carries log2(e)
+                if (p.softplus) g *= sigmoid_hw(w.v[i][e]);
+                ddt.set(e, g);
                 if (p.z) {
-                    const float z = w.z[i].v[e], sg = sigmoid_hw(z);
-                    dz[e] = w.dy[i].v[e] * fmaf(skip[e], x, o) * (sg * (1.0f + z * (1.0f - sg)));
+                    const float z = w.z[i].get(e), sg = sigmoid_hw(z);
+                    dz.set(e, w.dy[i].get(e) * fmaf(skip[e], x, o) * (sg * (1.0f + z * (1.0f - sg))));
                 }
                 if (e < n) {
                     dskip[e] = fmaf(ds, x, dskip[e]);
-                    dbias[e] += ddt[e];
+                    dbias[e] += g;
                 }
             }
             store_row4(dxp + t * p.dx_stride, dx, n);

@@ -8,60 +8,187 @@
 // a multiplication and an addition for each of the update's and the read-out's
 // products.  At N = 16 that arithmetic, not HBM, bounds it.
 //
-// A workgroup (scan_common.h) walks its rows in tiles of SCAN_ROWS.  Per tile
-//   stage     all threads load x, dt and z as 16-byte pieces of rows and put (s, s x)
-//             and (B, C) into LDS in fp32,
-//   scan      each wave runs its states through the tile's rows and leaves its part of
-//             each row's sum over n in LDS,
-//   epilogue  all threads add the parts, the skip and the gate and store y.
-// The next tile's loads are issued before the scan and arrive behind it.
+// A workgroup (scan_common.h) walks its rows in tiles of ROWS with two kinds of
+// waves, one of each on a SIMD:
+//   helpers   load x, dt and z of the tile after the next, put (s, s x) and (B, C) of the
+//             next tile into LDS in fp32, and finish the tile before: add the waves' parts
+//             of each row's sum over n, the skip and the gate, and store y;
+//   scanners  run their states through the tile's rows.
+// Both buffers in LDS are double, and one barrier per tile passes them on, so the scan,
+// whose rows depend on each other, always has a second instruction stream beside it.
 #include "scan_common.h"
 
 namespace mlstm {
 namespace {
 
-constexpr int SCAN_ROWS = 32;
-
 struct FwdParams {
     const void* x; const void* dt; const void* Bm; const void* Cm; const void* z;
     long long x_stride, dt_stride, B_stride, C_stride, z_stride, y_stride;
     const float* A; const float* Dskip; const float* dt_bias;
-    const int* seq_start; const float* h_init;
-    int S, rows, D, G, N, softplus;
-    int pieces, length;                  // pieces per sequence, rows per piece (a multiple of SCAN_ROWS)
+    const float* h_init;
+    Pieces pieces;
+    int D, G, N, softplus;
     void* y;
     float* h_final;
-    float* piece_h;                      // [B][pieces][NP][D]: end state of a piece that starts from zero
-    float* piece_s;                      // [B][pieces][D]: sum of its step sizes
+    float* piece_h;                      // [piece][NP][D]: end state of a piece that starts from zero
+    float* piece_s;                      // [piece][D]: sum of its step sizes
 };
 
 // STATE: only the piece's end state from zero (no y); else the full scan from the true state.
-template <typename T, int NW, int NL, bool STATE>
-__global__ __launch_bounds__(64 * NW) void scan_fwd_kernel(const FwdParams p)
+// GATE: y is gated by z.
+template <typename T, int NW, int NL, int ROWS, bool STATE, bool GATE>
+__global__ __launch_bounds__(128 * NW) void scan_fwd_kernel(const FwdParams p)
 {
-    constexpr int NT = 64 * NW, NP = NW * NL;
-    constexpr int PASS = SCAN_ROWS * 8 / NT;           // rows a thread stages per tile
-    constexpr int BCN = SCAN_ROWS * NP / NT;           // (B, C) pairs it stages
-    __shared__ __align__(16) float2 du[SCAN_ROWS][SCAN_TILE];
-    __shared__ __align__(16) float2 bc[SCAN_ROWS][NP];
-    __shared__ __align__(16) float part[STATE ? 1 : NW][SCAN_ROWS][SCAN_TILE];
+    constexpr int NT = 64 * NW, NP = NW * NL;          // helper threads, padded states
+    constexpr int PASS = ROWS * 16 / NT;          // rows a helper stages per tile, 4 channels each
+    constexpr int BCN = ROWS * NP / NT;           // (B, C) pairs it stages
+    __shared__ __align__(16) float2 du[2][ROWS][SCAN_TILE];
+    __shared__ __align__(16) float bs[2][ROWS][NP], cs[2][ROWS][NP];
+    __shared__ __align__(16) float part[STATE ? 1 : 2][STATE ? 1 : NW][ROWS][SCAN_TILE];
 
     const int tiles = scan_tiles(p.D, p.G);
-    const int pieces = STATE ? p.pieces - 1 : p.pieces;
-    const int tile = blockIdx.x % tiles;
-    const int c = (blockIdx.x / tiles) % pieces;
-    const int b = blockIdx.x / tiles / pieces;
-    const RowRange sq = sequence_rows(p.seq_start, b, p.S, p.rows);
-    const long long t_first = (long long)c * p.length;
+    const int tile = blockIdx.x % tiles, number = blockIdx.x / tiles;
+    const Pieces::At at = p.pieces.at(number);
+    const int b = at.b, c = at.c;
+    const RowRange sq = p.pieces.sequence(b);
+    const long long t_first = (long long)c * p.pieces.length;
     if (t_first >= sq.n && c > 0) return;
+    const bool last = t_first + p.pieces.length >= sq.n;       // the sequence ends in this piece
+    if (STATE && last) return;                                 // no other piece starts from its end
     const int t_begin = (int)t_first;
-    const int t_end = (int)min(t_first + p.length, (long long)sq.n);
+    const int t_end = last ? sq.n : t_begin + p.pieces.length;
+    const int turns = (t_end - t_begin + ROWS - 1) / ROWS;
     const ScanTile ch = scan_tile(tile, p.D, p.G);
+    const int lane = threadIdx.x & 63, wave = wave_id();
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
+    if (wave >= NW) {
+        // helper: rows r0 + (NT / 16) i of a tile, channels c4 .. c4 + 3.  Full tiles run
+        // without bounds checks, so that their loads, the finish of one tile and the
+        // staging of another interleave.
+        if (turns == 0) return;
+        const int tid = threadIdx.x - NT, r0 = tid >> 4, c4 = (tid & 15) * 4;
+        const long long row0 = sq.lo + t_begin + r0;
+        const T* xp = (const T*)p.x + row0 * p.x_stride + ch.d0 + c4;
+        const T* dtp = (const T*)p.dt + row0 * p.dt_stride + ch.d0 + c4;
+        const T* zp = GATE ? (const T*)p.z + row0 * p.z_stride + ch.d0 + c4 : nullptr;
+        T* yp = (T*)p.y + row0 * p.y_stride + ch.d0 + c4;
+        const int bt = tid / NP, bnn = tid % NP;
+        const T* bp = (const T*)p.Bm + (sq.lo + t_begin + bt) * p.B_stride + ch.group * p.N + bnn;
+        const T* cp = (const T*)p.Cm + (sq.lo + t_begin + bt) * p.C_stride + ch.group * p.N + bnn;
+        float bias[4], skip[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            bias[e] = p.dt_bias && c4 + e < ch.count ? p.dt_bias[ch.d0 + c4 + e] : 0.0f;
+            skip[e] = !STATE && p.Dskip && c4 + e < ch.count ? p.Dskip[ch.d0 + c4 + e] : 0.0f;
+        }
+        // x and z of the loaded tile, and of the staged one and the two before it
+        Raw4<T> xn[PASS], zn[PASS], dtn[PASS], x0[PASS], z0[PASS], x1[PASS], z1[PASS], x2[PASS], z2[PASS];
+        T bn[BCN], cn[BCN];
+        const bool full = ch.count == SCAN_TILE;
+        auto load = [&](int t0) {                      // the tile at t0; the pointers move on
+            const bool whole = full && t0 + ROWS <= t_end;
+#pragma unroll
+            for (int i = 0; i < PASS; ++i) {
+                const long long off = (NT / 16) * i;
+                if (whole) {
+                    xn[i].load(xp + off * p.x_stride);
+                    dtn[i].load(dtp + off * p.dt_stride);
+                    if (GATE) zn[i].load(zp + off * p.z_stride);
+                } else {
+                    const int n = t0 + r0 + off < t_end ? ch.count - c4 : 0;
+                    xn[i] = load_row4(xp + off * p.x_stride, n);
+                    dtn[i] = load_row4(dtp + off * p.dt_stride, n);
+                    if (GATE) zn[i] = load_row4(zp + off * p.z_stride, n);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < BCN; ++i) {
+                const long long off = (NT / NP) * i;
+                const bool live = t0 + bt + off < t_end && bnn < p.N;
+                bn[i] = live ? bp[off * p.B_stride] : from_f32<T>(0.0f);
+                if (!STATE) cn[i] = live ? cp[off * p.C_stride] : from_f32<T>(0.0f);
+            }
+            xp += ROWS * p.x_stride;
+            dtp += ROWS * p.dt_stride;
+            if (GATE) zp += ROWS * p.z_stride;
+            bp += ROWS * p.B_stride;
+            cp += ROWS * p.C_stride;
+        };
+        auto stage = [&](int t0, int buf) {
+#pragma unroll
+            for (int i = 0; i < PASS; ++i) {
+                const int r = r0 + (NT / 16) * i;
+                const bool row = t0 + r < t_end;       // past the end: decay 1, nothing added
+                float s[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] = dtn[i].get(e) + bias[e];
+                if (p.softplus)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[e] = softplus_hw(s[e]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] = row ? s[e] : 0.0f;
+                f32x4* to = reinterpret_cast<f32x4*>(&du[buf][r][c4]);
+                to[0] = f32x4{s[0], s[0] * xn[i].get(0), s[1], s[1] * xn[i].get(1)};
+                to[1] = f32x4{s[2], s[2] * xn[i].get(2), s[3], s[3] * xn[i].get(3)};
+                if (!STATE) {
+                    x2[i] = x1[i]; x1[i] = x0[i]; x0[i] = xn[i];
+                    if (GATE) { z2[i] = z1[i]; z1[i] = z0[i]; z0[i] = zn[i]; }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < BCN; ++i)
+            {
+                bs[buf][bt + (NT / NP) * i][bnn] = to_f32(bn[i]);
+                if (!STATE) cs[buf][bt + (NT / NP) * i][bnn] = to_f32(cn[i]);
+            }
+        };
+        auto finish = [&](int t0, int buf, const Raw4<T>* x, const Raw4<T>* z) {
+            const bool whole = full && t0 + ROWS <= t_end;
+#pragma unroll
+            for (int i = 0; i < PASS; ++i) {
+                const int r = r0 + (NT / 16) * i;
+                f32x4 y = *reinterpret_cast<const f32x4*>(&part[buf][0][r][c4]);
+#pragma unroll
+                for (int w = 1; w < NW; ++w) y += *reinterpret_cast<const f32x4*>(&part[buf][w][r][c4]);
+                Raw4<T> o;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    y[e] = fmaf(skip[e], x[i].get(e), y[e]);
+                    if (GATE) {
+                        const float zv = z[i].get(e);
+                        y[e] *= zv * sigmoid_hw(zv);
+                    }
+                    o.set(e, y[e]);
+                }
+                T* to = yp + (long long)(NT / 16) * i * p.y_stride;
+                if (whole) o.store(to);
+                else store_row4(to, o, t0 + r < t_end ? ch.count - c4 : 0);
+            }
+            yp += ROWS * p.y_stride;
+        };
+        load(t_begin);
+        stage(t_begin, 0);
+        if (turns > 1) load(t_begin + ROWS);
+        __syncthreads();
+        for (int i = 0; i < turns; ++i) {
+            const int t0 = t_begin + i * ROWS;
+            // the wait for the loads comes before the stores, whose completion it would wait for too
+            if (i + 1 < turns) {
+                stage(t0 + ROWS, (i + 1) & 1);
+                if (!STATE && i > 0) finish(t0 - ROWS, (i - 1) & 1, x2, z2);
+                if (i + 2 < turns) load(t0 + 2 * ROWS);
+            } else if (!STATE && i > 0) {
+                finish(t0 - ROWS, (i - 1) & 1, x1, z1);
+            }
+            __syncthreads();
+        }
+        if (!STATE) finish(t_begin + (turns - 1) * ROWS, (turns - 1) & 1, x0, z0);
+        return;
+    }
+
+    // scanner: channel d, states n0 .. n0 + NL - 1
     const int d = ch.d0 + lane, n0 = wave * NL;
     const bool own = lane < ch.count;
-
     float a2[NL], h[NL];
 #pragma unroll
     for (int j = 0; j < NL; ++j) {
@@ -71,116 +198,59 @@ __global__ __launch_bounds__(64 * NW) void scan_fwd_kernel(const FwdParams p)
     }
     if (!STATE && own) {
         // join: the states of the pieces before, each decayed by the sums of the step sizes behind it
-        for (int e = 0; e < c; ++e) {
-            const size_t at = (size_t)b * p.pieces + e;
-            const float sum = p.piece_s[at * p.D + d];
+        for (int e = number - c; e < number; ++e) {
+            const float sum = p.piece_s[(size_t)e * p.D + d];
 #pragma unroll
             for (int j = 0; j < NL; ++j)
-                h[j] = fmaf(__builtin_amdgcn_exp2f(a2[j] * sum), h[j], p.piece_h[(at * NP + n0 + j) * p.D + d]);
+                h[j] = fmaf(__builtin_amdgcn_exp2f(a2[j] * sum), h[j], p.piece_h[((size_t)e * NP + n0 + j) * p.D + d]);
         }
     }
-
-    // staging: this thread's rows r0 + (NT / 8) i of a tile, channels c8 .. c8 + 7
-    const int r0 = tid >> 3, c8 = (tid & 7) * 8;
-    const T* xp = (const T*)p.x + sq.lo * p.x_stride + ch.d0 + c8;
-    const T* dtp = (const T*)p.dt + sq.lo * p.dt_stride + ch.d0 + c8;
-    const T* zp = (const T*)p.z + (p.z ? sq.lo * p.z_stride + ch.d0 + c8 : 0);
-    T* yp = (T*)p.y + sq.lo * p.y_stride + ch.d0 + c8;
-    const T* bp = (const T*)p.Bm + sq.lo * p.B_stride + ch.group * p.N;
-    const T* cp = (const T*)p.Cm + sq.lo * p.C_stride + ch.group * p.N;
-    float bias[8], skip[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        bias[e] = p.dt_bias && c8 + e < ch.count ? p.dt_bias[ch.d0 + c8 + e] : 0.0f;
-        skip[e] = !STATE && p.Dskip && c8 + e < ch.count ? p.Dskip[ch.d0 + c8 + e] : 0.0f;
-    }
-    Raw8<T> xr[PASS], dtr[PASS], zr[PASS], xn[PASS], dtn[PASS], zn[PASS];
-    T br[BCN], cr[BCN];
-    auto load = [&](int t0) {
-#pragma unroll
-        for (int i = 0; i < PASS; ++i) {
-            const int t = t0 + r0 + (NT / 8) * i;
-            const int n = t < t_end ? ch.count - c8 : 0;
-            xn[i] = load_row8(xp + t * p.x_stride, n);
-            dtn[i] = load_row8(dtp + t * p.dt_stride, n);
-            if (!STATE && p.z) zn[i] = load_row8(zp + t * p.z_stride, n);
-        }
-#pragma unroll
-        for (int i = 0; i < BCN; ++i) {
-            const int at = tid + NT * i, t = t0 + at / NP, n = at % NP;
-            const bool live = t < t_end && n < p.N;
-            br[i] = live ? bp[t * p.B_stride + n] : from_f32<T>(0.0f);
-            if (!STATE) cr[i] = live ? cp[t * p.C_stride + n] : from_f32<T>(0.0f);
-        }
-    };
-
     float sums = 0.0f;                                 // of step sizes (STATE)
-    load(t_begin);
-    for (int t0 = t_begin; t0 < t_end; t0 += SCAN_ROWS) {
+    if (turns > 0) __syncthreads();
+    for (int i = 0; i < turns; ++i) {
+        const int buf = i & 1;
+        // rows in groups of four, the next group's operands read from LDS before this one's run
+        constexpr int GR = 4;
+        float2 su[2][GR];
+        float bv[2][GR], cv[2][GR][NL];
+        auto read = [&](int k, int g) {
 #pragma unroll
-        for (int i = 0; i < PASS; ++i) {
-            xr[i] = xn[i];
-            dtr[i] = dtn[i];
-            if (!STATE) zr[i] = zn[i];
-            const int r = r0 + (NT / 8) * i;
-            const bool row = t0 + r < t_end;           // past the end: decay 1, nothing added
+            for (int r = 0; r < GR; ++r) {
+                su[k][r] = du[buf][g + r][lane];
+                bv[k][r] = bs[buf][g + r][n0 + (lane & (NL - 1))];
+                if (!STATE)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float v = dtr[i].get(e) + bias[e];
-                const float s = row ? (p.softplus ? softplus_hw(v) : v) : 0.0f;
-                du[r][c8 + e] = float2{s, s * xr[i].get(e)};
+                    for (int j = 0; j < NL; j += 4)
+                        *reinterpret_cast<f32x4*>(cv[k][r] + j) = *reinterpret_cast<const f32x4*>(&cs[buf][g + r][n0 + j]);
+            }
+        };
+        read(0, 0);
+#pragma unroll
+        for (int g = 0; g < ROWS; g += GR) {
+            const int k = g / GR & 1;
+            if (g + GR < ROWS) read(k ^ 1, g + GR);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int r = 0; r < GR; ++r) {
+                float y = 0.0f;
+                for_each<NL>([&](auto jc) {
+                    constexpr int j = jc;
+                    const float a = __builtin_amdgcn_exp2f(su[k][r].x * a2[j]);
+                    h[j] = fmaf(a, h[j], row_broadcast<j>(bv[k][r]) * su[k][r].y);
+                    if (!STATE) y = j == 0 ? cv[k][r][0] * h[0] : fmaf(cv[k][r][j], h[j], y);
+                });
+                if (STATE) sums += su[k][r].x;
+                else part[buf][wave][g + r][lane] = y;
             }
         }
-#pragma unroll
-        for (int i = 0; i < BCN; ++i) {
-            const int at = tid + NT * i;
-            bc[at / NP][at % NP] = float2{to_f32(br[i]), STATE ? 0.0f : to_f32(cr[i])};
-        }
         __syncthreads();
-        if (t0 + SCAN_ROWS < t_end) load(t0 + SCAN_ROWS);
-#pragma unroll 4
-        for (int t = 0; t < SCAN_ROWS; ++t) {
-            const float2 su = du[t][lane];
-            const float2 bcv = bc[t][n0 + (lane & (NL - 1))];
-            float y = 0.0f;
-            for_each<NL>([&](auto jc) {
-                constexpr int j = jc;
-                const float a = __builtin_amdgcn_exp2f(su.x * a2[j]);
-                h[j] = fmaf(a, h[j], row_broadcast<j>(bcv.x) * su.y);
-                if (!STATE) y = fmaf(row_broadcast<j>(bcv.y), h[j], y);
-            });
-            if (STATE) sums += su.x;
-            else part[wave][t][lane] = y;
-        }
-        __syncthreads();
-        if (!STATE) {
-#pragma unroll
-            for (int i = 0; i < PASS; ++i) {
-                const int r = r0 + (NT / 8) * i, t = t0 + r;
-                Raw8<T> o;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float y = part[0][r][c8 + e];
-#pragma unroll
-                    for (int w = 1; w < NW; ++w) y += part[w][r][c8 + e];
-                    y = fmaf(skip[e], xr[i].get(e), y);
-                    if (p.z) {
-                        const float z = zr[i].get(e);
-                        y *= z * sigmoid_hw(z);
-                    }
-                    o.set(e, y);
-                }
-                store_row8(yp + t * p.y_stride, o, t < t_end ? ch.count - c8 : 0);
-            }
-        }
     }
     if (!own) return;
     if (STATE) {
-        const size_t at = (size_t)b * p.pieces + c;
 #pragma unroll
-        for (int j = 0; j < NL; ++j) p.piece_h[(at * NP + n0 + j) * p.D + d] = h[j];
-        if (wave == 0) p.piece_s[at * p.D + d] = sums;
-    } else if (p.h_final && t_first + p.length >= sq.n) {      // the sequence ends in this piece
+        for (int j = 0; j < NL; ++j) p.piece_h[((size_t)number * NP + n0 + j) * p.D + d] = h[j];
+        if (wave == 0) p.piece_s[(size_t)number * p.D + d] = sums;
+    } else if (p.h_final && last) {
 #pragma unroll
         for (int j = 0; j < NL; ++j)
             if (n0 + j < p.N) p.h_final[((size_t)b * p.D + d) * p.N + n0 + j] = h[j];
@@ -245,38 +315,68 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(
     }
 }
 
-// Pieces of a sequence.  One piece does the least work (the pieces' end states cost
-// most of the scan a second time), so a sequence is cut only where its workgroups
-// leave compute units idle.
-struct FwdPlan { int pieces, length; };
-FwdPlan plan(int B, int S, int D, int G) {
-    (void)B; (void)D; (void)G;
-    return FwdPlan{1, (S + SCAN_ROWS - 1) / SCAN_ROWS * SCAN_ROWS};
+// Rows per piece.  One piece to a sequence does the least work: where sequences are
+// cut, the pieces' end states cost most of the scan a second time.  A workgroup alone on its
+// compute unit takes about 70 ns a row; cut into about three workgroups per compute unit the scan
+// takes 7.2 ps per row and channel against 4.2 uncut.  So sequences are cut below 144
+// workgroups: on one MI355X (2, 1024, 4096) (sequences, rows, channels; 128 workgroups) took
+// 76 us uncut and 67 us in six pieces, (8, 2048, 1536) (192 workgroups) 148 us uncut and 173 us
+// in eight; (1, 32768, 2048) 2512 us uncut, 646, 501, 483 and 499 us in 8, 16, 32 and 64 pieces.
+constexpr int CUT_BELOW = 144, CUT_TO = 768, SHORTEST_PIECE = 64;
+int piece_rows(int S, int rows, int D, int G) {
+    // packed sequences count by the rows that there are
+    const long long groups = (long long)scan_tiles(D, G) * ((rows + S - 1) / S);
+    const int whole = (S + 31) / 32 * 32;
+    if (groups > CUT_BELOW) return whole;
+    const long long n = (CUT_TO + groups - 1) / groups;
+    const int length = (int)(((S + n - 1) / n + 15) / 16 * 16);
+    return length < SHORTEST_PIECE ? (SHORTEST_PIECE < whole ? SHORTEST_PIECE : whole) : length;
 }
-size_t piece_h_elems(const FwdPlan& f, int B, int D, int N) {
-    return (size_t)B * f.pieces * scan_padded_states(N) * D;
+
+struct FwdPlan {
+    Pieces pieces;
+    size_t state;                        // floats of piece_h (piece_s lies behind them); 0: uncut
+    size_t total;
+};
+FwdPlan plan(const int* seq_start, int B, int S, int rows, int D, int G, int N) {
+    FwdPlan f = {};
+    f.pieces = make_pieces(seq_start, B, S, rows, piece_rows(S, rows, D, G));
+    if (f.pieces.length < S) {
+        // as many as packed sequences may need, so that a workspace's size does not depend on seq_start
+        const size_t count = (size_t)rows / f.pieces.length + B;
+        f.state = count * scan_padded_states(N) * D;
+        f.total = f.state + count * D;
+    }
+    return f;
 }
 
 template <typename T>
 hipError_t fwd_t(const ScanArgs& a) {
-    const FwdPlan f = plan(a.B, a.S, a.D, a.G);
+    const FwdPlan f = plan(a.seq_start, a.B, a.S, a.rows, a.D, a.G, a.N);
     FwdParams p = {};
     p.x = a.x; p.dt = a.dt; p.Bm = a.Bm; p.Cm = a.Cm; p.z = a.z;
     p.x_stride = a.x_stride; p.dt_stride = a.dt_stride; p.B_stride = a.B_stride; p.C_stride = a.C_stride;
     p.z_stride = a.z_stride; p.y_stride = a.y_stride;
-    p.A = a.A; p.Dskip = a.Dskip; p.dt_bias = a.dt_bias; p.seq_start = a.seq_start; p.h_init = a.h_init;
-    p.S = a.S; p.rows = a.rows; p.D = a.D; p.G = a.G; p.N = a.N; p.softplus = a.softplus;
-    p.pieces = f.pieces; p.length = f.length;
+    p.A = a.A; p.Dskip = a.Dskip; p.dt_bias = a.dt_bias; p.h_init = a.h_init; p.pieces = f.pieces;
+    p.D = a.D; p.G = a.G; p.N = a.N; p.softplus = a.softplus;
     p.y = a.y; p.h_final = a.h_final;
-    p.piece_h = a.ws; p.piece_s = a.ws + piece_h_elems(f, a.B, a.D, a.N);
-    const unsigned per = (unsigned)scan_tiles(a.D, a.G) * a.B;
-#define SCAN_CALL(NW, NL)                                                                                              \
-    if (f.pieces > 1)                                                                                                  \
-        hipLaunchKernelGGL((scan_fwd_kernel<T, NW, NL, true>), dim3(per * (f.pieces - 1)), dim3(64 * NW), 0, a.stream, \
-                           p);                                                                                         \
-    hipLaunchKernelGGL((scan_fwd_kernel<T, NW, NL, false>), dim3(per * f.pieces), dim3(64 * NW), 0, a.stream, p)
+    p.piece_h = a.ws; p.piece_s = a.ws + f.state;
+    const unsigned grid = (unsigned)scan_tiles(a.D, a.G) * f.pieces.count();
+    // Tiles of 32 rows have half the barriers but take 104 KB of LDS, one workgroup to a compute
+    // unit; of 16 rows three fit.  (4, 2048, 4096), 256 workgroups, uncut: 157 us against 177 us;
+    // (16, 1024, 2048), 512 workgroups: 165 us against 139 us.
+    const bool deep = !f.state && grid <= 256;
+#define SCAN_LAUNCH(NW, NL, ROWS, STATE, GATE) \
+    hipLaunchKernelGGL((scan_fwd_kernel<T, NW, NL, ROWS, STATE, GATE>), dim3(grid), dim3(128 * NW), 0, a.stream, p)
+#define SCAN_CALL(NW, NL)                                    \
+    if (f.state) SCAN_LAUNCH(NW, NL, 16, true, false);       \
+    if (deep && a.z) SCAN_LAUNCH(NW, NL, 32, false, true);   \
+    else if (deep) SCAN_LAUNCH(NW, NL, 32, false, false);    \
+    else if (a.z) SCAN_LAUNCH(NW, NL, 16, false, true);      \
+    else SCAN_LAUNCH(NW, NL, 16, false, false)
     SCAN_DISPATCH_N(a.N, SCAN_CALL)
 #undef SCAN_CALL
+#undef SCAN_LAUNCH
     return hipGetLastError();
 }
 
@@ -301,10 +401,8 @@ hipError_t step_t(const ScanArgs& a) {
 
 }  // namespace
 
-size_t scan_fwd_workspace_bytes(int B, int S, int D, int G, int N) {
-    const FwdPlan f = plan(B, S, D, G);
-    if (f.pieces == 1) return 0;
-    return (piece_h_elems(f, B, D, N) + (size_t)B * f.pieces * D) * sizeof(float);
+size_t scan_fwd_workspace_bytes(int B, int S, int rows, int D, int G, int N) {
+    return plan(nullptr, B, S, rows, D, G, N).total * sizeof(float);
 }
 
 hipError_t launch_scan_fwd(const ScanArgs& a) {

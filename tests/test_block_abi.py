@@ -171,11 +171,11 @@ def test_scan_refusals(lib, kw, words):
 
 def test_scan_workspace(lib):
     big = dict(B=1, S=65536, rows=65536)
-    need = b.ssm_scan_fwd_workspace_bytes(1, 65536, 64, 1, 16)
-    if need:
-        refused(_scan(lib, n=need - 1, **big), "needed", b.MLSTM_ERR_WORKSPACE)
-        refused(_scan(lib, ws=P[11] + 4, **big), "workspace is not 16-byte aligned")
-    for bad in ((0, 8, 64, 1, 16), (2, 0, 64, 1, 16), (2, 8, 64, 3, 16), (2, 8, 64, 1, 65)):
+    need = b.ssm_scan_fwd_workspace_bytes(1, 65536, 65536, 64, 1, 16)
+    assert need > 0
+    refused(_scan(lib, n=need - 1, **big), "needed", b.MLSTM_ERR_WORKSPACE)
+    refused(_scan(lib, ws=P[11] + 4, **big), "workspace is not 16-byte aligned")
+    for bad in ((0, 8, 16, 64, 1, 16), (2, 0, 16, 64, 1, 16), (2, 8, 16, 64, 3, 16), (2, 8, 16, 64, 1, 65), (2, 8, 0, 64, 1, 16)):
         assert b.ssm_scan_fwd_workspace_bytes(*bad) == 0
 
 
