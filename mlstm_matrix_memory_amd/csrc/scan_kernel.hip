@@ -62,127 +62,140 @@ __global__ __launch_bounds__(128 * NW) void scan_fwd_kernel(const FwdParams p)
     const int lane = threadIdx.x & 63, wave = wave_id();
 
     if (wave >= NW) {
-        // helper: rows r0 + (NT / 16) i of a tile, channels c4 .. c4 + 3.  Full tiles run
-        // without bounds checks, so that their loads, the finish of one tile and the
-        // staging of another interleave.
+        // helper: rows r0 + (NT / 16) i of a tile, channels c4 .. c4 + 3
         if (turns == 0) return;
         const int tid = threadIdx.x - NT, r0 = tid >> 4, c4 = (tid & 15) * 4;
-        const long long row0 = sq.lo + t_begin + r0;
-        const T* xp = (const T*)p.x + row0 * p.x_stride + ch.d0 + c4;
-        const T* dtp = (const T*)p.dt + row0 * p.dt_stride + ch.d0 + c4;
-        const T* zp = GATE ? (const T*)p.z + row0 * p.z_stride + ch.d0 + c4 : nullptr;
-        T* yp = (T*)p.y + row0 * p.y_stride + ch.d0 + c4;
         const int bt = tid / NP, bnn = tid % NP;
-        const T* bp = (const T*)p.Bm + (sq.lo + t_begin + bt) * p.B_stride + ch.group * p.N + bnn;
-        const T* cp = (const T*)p.Cm + (sq.lo + t_begin + bt) * p.C_stride + ch.group * p.N + bnn;
+        const T* xp = (const T*)p.x + (long long)sq.lo * p.x_stride + ch.d0 + c4;
+        const T* dtp = (const T*)p.dt + (long long)sq.lo * p.dt_stride + ch.d0 + c4;
+        const T* zp = GATE ? (const T*)p.z + (long long)sq.lo * p.z_stride + ch.d0 + c4 : nullptr;
+        T* yp = (T*)p.y + (long long)sq.lo * p.y_stride + ch.d0 + c4;
+        const T* bp = (const T*)p.Bm + (long long)sq.lo * p.B_stride + ch.group * p.N + min(bnn, p.N - 1);
+        const T* cp = (const T*)p.Cm + (long long)sq.lo * p.C_stride + ch.group * p.N + min(bnn, p.N - 1);
         float bias[4], skip[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             bias[e] = p.dt_bias && c4 + e < ch.count ? p.dt_bias[ch.d0 + c4 + e] : 0.0f;
             skip[e] = !STATE && p.Dskip && c4 + e < ch.count ? p.Dskip[ch.d0 + c4 + e] : 0.0f;
         }
-        // x and z of the loaded tile, and of the staged one and the two before it
-        Raw4<T> xn[PASS], zn[PASS], dtn[PASS], x0[PASS], z0[PASS], x1[PASS], z1[PASS], x2[PASS], z2[PASS];
-        T bn[BCN], cn[BCN];
-        const bool full = ch.count == SCAN_TILE;
-        auto load = [&](int t0) {                      // the tile at t0; the pointers move on
-            const bool whole = full && t0 + ROWS <= t_end;
+        // Loads run two tiles ahead.  To know how many accesses lie between a load and its
+        // use, and so wait for no later ones, the compiler needs every turn to issue the
+        // same: rows past the end are read from the last row and masked when staged.
+        auto work = [&](auto full_tag) {
+            constexpr bool FULL = full_tag;            // the tile holds all of its 64 channels
+            const int nc = FULL ? 4 : ch.count - c4;
+            Raw4<T> xn[2][PASS], zn[2][PASS], dtn[2][PASS];
+            T bn[2][BCN], cn[2][BCN];
+            // x and z of the staged tile and the two before it
+            Raw4<T> x0[PASS], z0[PASS], x1[PASS], z1[PASS], x2[PASS], z2[PASS];
+            auto get = [&](const T* q) {
+                Raw4<T> v;
+                if (FULL) v.load(q);
+                else v = load_row4(q, nc);
+                return v;
+            };
+            auto load = [&](int turn, auto kc) {
+                constexpr int k = kc;
+                const int t0 = t_begin + min(turn, turns - 1) * ROWS;
 #pragma unroll
-            for (int i = 0; i < PASS; ++i) {
-                const long long off = (NT / 16) * i;
-                if (whole) {
-                    xn[i].load(xp + off * p.x_stride);
-                    dtn[i].load(dtp + off * p.dt_stride);
-                    if (GATE) zn[i].load(zp + off * p.z_stride);
-                } else {
-                    const int n = t0 + r0 + off < t_end ? ch.count - c4 : 0;
-                    xn[i] = load_row4(xp + off * p.x_stride, n);
-                    dtn[i] = load_row4(dtp + off * p.dt_stride, n);
-                    if (GATE) zn[i] = load_row4(zp + off * p.z_stride, n);
+                for (int i = 0; i < PASS; ++i) {
+                    const long long t = min(t0 + r0 + (NT / 16) * i, t_end - 1);
+                    xn[k][i] = get(xp + t * p.x_stride);
+                    dtn[k][i] = get(dtp + t * p.dt_stride);
+                    if (GATE) zn[k][i] = get(zp + t * p.z_stride);
                 }
-            }
 #pragma unroll
-            for (int i = 0; i < BCN; ++i) {
-                const long long off = (NT / NP) * i;
-                const bool live = t0 + bt + off < t_end && bnn < p.N;
-                bn[i] = live ? bp[off * p.B_stride] : from_f32<T>(0.0f);
-                if (!STATE) cn[i] = live ? cp[off * p.C_stride] : from_f32<T>(0.0f);
-            }
-            xp += ROWS * p.x_stride;
-            dtp += ROWS * p.dt_stride;
-            if (GATE) zp += ROWS * p.z_stride;
-            bp += ROWS * p.B_stride;
-            cp += ROWS * p.C_stride;
-        };
-        auto stage = [&](int t0, int buf) {
-#pragma unroll
-            for (int i = 0; i < PASS; ++i) {
-                const int r = r0 + (NT / 16) * i;
-                const bool row = t0 + r < t_end;       // past the end: decay 1, nothing added
-                float s[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[e] = dtn[i].get(e) + bias[e];
-                if (p.softplus)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[e] = softplus_hw(s[e]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[e] = row ? s[e] : 0.0f;
-                f32x4* to = reinterpret_cast<f32x4*>(&du[buf][r][c4]);
-                to[0] = f32x4{s[0], s[0] * xn[i].get(0), s[1], s[1] * xn[i].get(1)};
-                to[1] = f32x4{s[2], s[2] * xn[i].get(2), s[3], s[3] * xn[i].get(3)};
-                if (!STATE) {
-                    x2[i] = x1[i]; x1[i] = x0[i]; x0[i] = xn[i];
-                    if (GATE) { z2[i] = z1[i]; z1[i] = z0[i]; z0[i] = zn[i]; }
+                for (int i = 0; i < BCN; ++i) {
+                    const long long t = min(t0 + bt + (NT / NP) * i, t_end - 1);
+                    bn[k][i] = bp[t * p.B_stride];
+                    if (!STATE) cn[k][i] = cp[t * p.C_stride];
                 }
-            }
+            };
+            auto stage = [&](int turn, auto kc) {
+                constexpr int k = kc;
+                const int t0 = t_begin + turn * ROWS, buf = turn & 1;
 #pragma unroll
-            for (int i = 0; i < BCN; ++i)
-            {
-                bs[buf][bt + (NT / NP) * i][bnn] = to_f32(bn[i]);
-                if (!STATE) cs[buf][bt + (NT / NP) * i][bnn] = to_f32(cn[i]);
-            }
-        };
-        auto finish = [&](int t0, int buf, const Raw4<T>* x, const Raw4<T>* z) {
-            const bool whole = full && t0 + ROWS <= t_end;
+                for (int i = 0; i < PASS; ++i) {
+                    const int r = r0 + (NT / 16) * i;
+                    const bool row = t0 + r < t_end;   // past the end: decay 1, nothing added
+                    float s[4], u[4];
 #pragma unroll
-            for (int i = 0; i < PASS; ++i) {
-                const int r = r0 + (NT / 16) * i;
-                f32x4 y = *reinterpret_cast<const f32x4*>(&part[buf][0][r][c4]);
+                    for (int e = 0; e < 4; ++e) s[e] = dtn[k][i].get(e) + bias[e];
+                    if (p.softplus)
 #pragma unroll
-                for (int w = 1; w < NW; ++w) y += *reinterpret_cast<const f32x4*>(&part[buf][w][r][c4]);
-                Raw4<T> o;
+                        for (int e = 0; e < 4; ++e) s[e] = softplus_hw(s[e]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    y[e] = fmaf(skip[e], x[i].get(e), y[e]);
-                    if (GATE) {
-                        const float zv = z[i].get(e);
-                        y[e] *= zv * sigmoid_hw(zv);
+                    for (int e = 0; e < 4; ++e) {
+                        u[e] = row ? s[e] * xn[k][i].get(e) : 0.0f;
+                        s[e] = row ? s[e] : 0.0f;
                     }
-                    o.set(e, y[e]);
+                    f32x4* to = reinterpret_cast<f32x4*>(&du[buf][r][c4]);
+                    to[0] = f32x4{s[0], u[0], s[1], u[1]};
+                    to[1] = f32x4{s[2], u[2], s[3], u[3]};
+                    if (!STATE) {
+                        x2[i] = x1[i]; x1[i] = x0[i]; x0[i] = xn[k][i];
+                        if (GATE) { z2[i] = z1[i]; z1[i] = z0[i]; z0[i] = zn[k][i]; }
+                    }
                 }
-                T* to = yp + (long long)(NT / 16) * i * p.y_stride;
-                if (whole) o.store(to);
-                else store_row4(to, o, t0 + r < t_end ? ch.count - c4 : 0);
-            }
-            yp += ROWS * p.y_stride;
-        };
-        load(t_begin);
-        stage(t_begin, 0);
-        if (turns > 1) load(t_begin + ROWS);
-        __syncthreads();
-        for (int i = 0; i < turns; ++i) {
-            const int t0 = t_begin + i * ROWS;
-            // the wait for the loads comes before the stores, whose completion it would wait for too
-            if (i + 1 < turns) {
-                stage(t0 + ROWS, (i + 1) & 1);
-                if (!STATE && i > 0) finish(t0 - ROWS, (i - 1) & 1, x2, z2);
-                if (i + 2 < turns) load(t0 + 2 * ROWS);
-            } else if (!STATE && i > 0) {
-                finish(t0 - ROWS, (i - 1) & 1, x1, z1);
-            }
+#pragma unroll
+                for (int i = 0; i < BCN; ++i) {
+                    const int r = bt + (NT / NP) * i;
+                    const bool live = t0 + r < t_end && bnn < p.N;
+                    bs[buf][r][bnn] = live ? to_f32(bn[k][i]) : 0.0f;
+                    if (!STATE) cs[buf][r][bnn] = live ? to_f32(cn[k][i]) : 0.0f;
+                }
+            };
+            auto finish = [&](int turn, const Raw4<T>* x, const Raw4<T>* z) {
+                const int t0 = t_begin + turn * ROWS, buf = turn & 1;
+#pragma unroll
+                for (int i = 0; i < PASS; ++i) {
+                    const int r = r0 + (NT / 16) * i;
+                    const long long t = t0 + r;
+                    f32x4 y = *reinterpret_cast<const f32x4*>(&part[buf][0][r][c4]);
+#pragma unroll
+                    for (int w = 1; w < NW; ++w) y += *reinterpret_cast<const f32x4*>(&part[buf][w][r][c4]);
+                    Raw4<T> o;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        y[e] = fmaf(skip[e], x[i].get(e), y[e]);
+                        if (GATE) {
+                            const float zv = z[i].get(e);
+                            y[e] *= zv * sigmoid_hw(zv);
+                        }
+                        o.set(e, y[e]);
+                    }
+                    if (t < t_end) {
+                        if (FULL) o.store(yp + t * p.y_stride);
+                        else store_row4(yp + t * p.y_stride, o, nc);
+                    }
+                }
+            };
+            typedef std::integral_constant<int, 0> Even;
+            typedef std::integral_constant<int, 1> Odd;
+            load(0, Even());
+            load(1, Odd());
+            stage(0, Even());
+            load(2, Even());
             __syncthreads();
-        }
-        if (!STATE) finish(t_begin + (turns - 1) * ROWS, (turns - 1) & 1, x0, z0);
+            // turn i: tile i is scanned, i + 1 staged and i - 1 finished
+            auto turn = [&](int i, auto next) {
+                if (i + 1 < turns) {
+                    stage(i + 1, next);
+                    if (!STATE && i > 0) finish(i - 1, x2, z2);
+                } else if (!STATE && i > 0) {
+                    finish(i - 1, x1, z1);
+                }
+                load(i + 3, next);
+                __syncthreads();
+            };
+            for (int i = 0; i < turns; i += 2) {
+                turn(i, Odd());
+                if (i + 1 < turns) turn(i + 1, Even());
+            }
+            if (!STATE) finish(turns - 1, x0, z0);
+        };
+        if (ch.count == SCAN_TILE) work(std::true_type());
+        else work(std::false_type());
         return;
     }
 
