@@ -211,6 +211,7 @@ __global__ __launch_bounds__(128 * NW) void scan_fwd_kernel(const FwdParams p)
     }
     if (!STATE && own) {
         // join: the states of the pieces before, each decayed by the sums of the step sizes behind it
+#pragma unroll 4
         for (int e = number - c; e < number; ++e) {
             const float sum = p.piece_s[(size_t)e * p.D + d];
 #pragma unroll
@@ -330,12 +331,12 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(
 
 // Rows per piece.  One piece to a sequence does the least work: where sequences are
 // cut, the pieces' end states cost most of the scan a second time.  A workgroup alone on its
-// compute unit takes about 70 ns a row; cut into about three workgroups per compute unit the scan
+// compute unit takes about 70 ns a row; cut into some workgroups per compute unit the scan
 // takes 7.2 ps per row and channel against 4.2 uncut.  So sequences are cut below 144
 // workgroups: on one MI355X (2, 1024, 4096) (sequences, rows, channels; 128 workgroups) took
 // 76 us uncut and 67 us in six pieces, (8, 2048, 1536) (192 workgroups) 148 us uncut and 173 us
 // in eight; (1, 32768, 2048) 2512 us uncut, 646, 501, 483 and 499 us in 8, 16, 32 and 64 pieces.
-constexpr int CUT_BELOW = 144, CUT_TO = 768, SHORTEST_PIECE = 64;
+constexpr int CUT_BELOW = 144, CUT_TO = 1024, SHORTEST_PIECE = 64;
 int piece_rows(int S, int rows, int D, int G) {
     // packed sequences count by the rows that there are
     const long long groups = (long long)scan_tiles(D, G) * ((rows + S - 1) / S);
