@@ -14,10 +14,15 @@
 // states in registers.  Arithmetic bounds both: per (row, channel, state) an exponential
 // and 3 vector instructions forward, twice, and about 11 back.
 //
-// The sums over channels (dB, dC) run across the lanes: each wave leaves the products
-// of two rows in LDS and adds them with wide reads, one addition per product, which
-// costs a fifth of a lane-exchange tree.  A tile of channels writes its sums to the
-// workspace, and a last kernel adds the tiles (no atomics).
+// In the second kernel a lane holds 4 states (or several times 4, one after the other)
+// of a channel, and LPC = NP / 4, at most 4, neighbouring lanes a channel.  The sums over
+// a channel's states (read-out, du, sum_n A w) then take two additions with the DPP lane
+// permutation, and the sums over the wave's channels (dB, dC) run as a
+// halving exchange between lanes: the permlane swaps add two values in one addition.  Both
+// stay in registers, free to overlap with the next rows' arithmetic; through LDS, with the
+// states of a channel in four waves, the same kernel took 1.4 times as long, waiting for LDS.
+// A tile of channels writes its sums to the workspace, and a last kernel adds the
+// tiles (no atomics).
 //
 // A sequence that fills too little of the chip is cut into pieces.  The first kernel then
 // starts every piece but a sequence's first from zero and also leaves the gradient
@@ -26,12 +31,12 @@
 // piece reaches the state k rows on by the factor exp(A (s_0 + ... + s_k)), so the second
 // kernel adds it to the kept states, and joins the R of the pieces behind.
 #include "scan_common.h"
-#include <stdlib.h>
 
 namespace mlstm {
 namespace {
 
-constexpr int BWD_ROWS = 16;
+constexpr int BWD_ROWS = 16;                     // rows staged at a time
+constexpr int KEEP = 8;                          // rows between kept states
 
 struct BwdParams {
     const void* x; const void* dt; const void* Bm; const void* Cm; const void* z; const void* dy;
@@ -52,8 +57,8 @@ struct BwdParams {
 };
 
 // where a sequence's tiles of rows start among the slots of `state`: no two sequences share
-// one, and rows / BWD_ROWS + B slots hold them all
-__device__ __forceinline__ int first_slot(const RowRange& sq, int b) { return sq.lo / BWD_ROWS + b; }
+// one, and rows / KEEP + B slots hold them all
+__device__ __forceinline__ int first_slot(const RowRange& sq, int b) { return sq.lo / KEEP + b; }
 
 // The piece, channel tile and rows of a workgroup, and its threads' part in staging
 // a tile of rows: thread -> row tid / 16 (+ NT / 16 i), channels 4 (tid % 16) .. + 3.
@@ -65,7 +70,7 @@ struct Work {
     struct Lds {
         float2 su[BWD_ROWS][SCAN_TILE];                // step size, step size * x
         float ds[BWD_ROWS][SCAN_TILE];
-        float2 bc[BWD_ROWS][NP];                       // B, C
+        float bs[BWD_ROWS][NP], cs[BWD_ROWS][NP];      // B, C
     };
 
     const BwdParams& p;
@@ -180,7 +185,10 @@ struct Work {
 #pragma unroll
         for (int i = 0; i < BCN; ++i) {
             const int at = tid + NT * i;
-            if (at < BWD_ROWS * NP) l.bc[at / NP][at % NP] = float2{to_f32(bn[i]), GRAD ? to_f32(cn[i]) : 0.0f};
+            if (at < BWD_ROWS * NP) {
+                l.bs[at / NP][at % NP] = to_f32(bn[i]);
+                if (GRAD) l.cs[at / NP][at % NP] = to_f32(cn[i]);
+            }
         }
     }
 };
@@ -205,31 +213,33 @@ __global__ __launch_bounds__(64 * NW) void scan_bwd_states_kernel(const BwdParam
     }
     if (w.t_begin < w.t_end) w.template load<CUT>(w.t_begin);
     for (int t0 = w.t_begin; t0 < w.t_end; t0 += BWD_ROWS) {
-        if (w.own) {
-            const size_t slot = w.slot + t0 / BWD_ROWS;
-#pragma unroll
-            for (int j = 0; j < NL; ++j) p.state[(slot * W::NP + w.n0 + j) * p.D + w.d] = h[j];
-            if (CUT && w.wave == 0) p.before[slot * p.D + w.d] = sum;
-        }
-        if (!CUT && t0 + BWD_ROWS >= w.t_end) break;   // the last tile's end state is not needed
         w.template put<CUT>(lds, t0);
         __syncthreads();
         if (t0 + BWD_ROWS < w.t_end) w.template load<CUT>(t0 + BWD_ROWS);
-#pragma unroll 4
-        for (int t = 0; t < BWD_ROWS; ++t) {
-            const float2 su = lds.su[t][w.lane];
-            const float ds = CUT ? lds.ds[t][w.lane] : 0.0f;
-            const float2 bcv = lds.bc[t][w.n0 + (w.lane & (NL - 1))];
-            sum += su.x;
-            for_each<NL>([&](auto jc) {
-                constexpr int j = jc;
-                const float a = __builtin_amdgcn_exp2f(su.x * a2[j]);
-                h[j] = fmaf(a, h[j], row_broadcast<j>(bcv.x) * su.y);
-                if (CUT) {
-                    prod[j] *= a;
-                    R[j] = fmaf(prod[j], row_broadcast<j>(bcv.y) * ds, R[j]);
-                }
-            });
+        for (int half = 0; half < BWD_ROWS; half += KEEP) {
+            if (w.own && t0 + half < w.t_end) {
+                const size_t slot = w.slot + (t0 + half) / KEEP;
+#pragma unroll
+                for (int j = 0; j < NL; ++j) p.state[(slot * W::NP + w.n0 + j) * p.D + w.d] = h[j];
+                if (CUT && w.wave == 0) p.before[slot * p.D + w.d] = sum;
+            }
+#pragma unroll
+            for (int t = 0; t < KEEP; ++t) {
+                const float2 su = lds.su[half + t][w.lane];
+                const float ds = CUT ? lds.ds[half + t][w.lane] : 0.0f;
+                const int at = w.n0 + (w.lane & (NL - 1));
+                const float bv = lds.bs[half + t][at], cv = CUT ? lds.cs[half + t][at] : 0.0f;
+                sum += su.x;
+                for_each<NL>([&](auto jc) {
+                    constexpr int j = jc;
+                    const float a = __builtin_amdgcn_exp2f(su.x * a2[j]);
+                    h[j] = fmaf(a, h[j], row_broadcast<j>(bv) * su.y);
+                    if (CUT) {
+                        prod[j] *= a;
+                        R[j] = fmaf(prod[j], row_broadcast<j>(cv) * ds, R[j]);
+                    }
+                });
+            }
         }
         __syncthreads();
     }
@@ -243,44 +253,71 @@ __global__ __launch_bounds__(64 * NW) void scan_bwd_states_kernel(const BwdParam
     if (w.wave == 0) p.piece_s[at * p.D + w.d] = sum;
 }
 
+// x + x of lane ^ M (M = 1 or 2)
+template <int M>
+__device__ __forceinline__ float add_xor(float x) {
+    constexpr int perm = M == 1 ? 0xB1 : 0x4E;         // quad_perm [1,0,3,2], [2,3,0,1]
+    return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), perm, 0xF, 0xF, true));
+}
+// x + x of the lane R further on (in a ring) in its row of 16
+template <int R>
+__device__ __forceinline__ float add_ror(float x) {
+    return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x120 + R, 0xF, 0xF, true));
+}
+// lanes 0..31: the sum of a over lanes l and l + 32; lanes 32..63: of b
+__device__ __forceinline__ float add_halves(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b), false, false);
+    return __builtin_bit_cast(float, (unsigned)r[0]) + __builtin_bit_cast(float, (unsigned)r[1]);
+}
+// even rows of 16 lanes: the sum of a over that row and the next; odd rows: of b over the one before and that
+__device__ __forceinline__ float add_rows(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b), false, false);
+    return __builtin_bit_cast(float, (unsigned)r[0]) + __builtin_bit_cast(float, (unsigned)r[1]);
+}
+
 template <typename T, int NW, int NL, bool CUT>
-__global__ __launch_bounds__(64 * NW, 2) void scan_bwd_kernel(const BwdParams p)
+__global__ __launch_bounds__(64 * NW, NW == 4 && NL == 4 ? 2 : 1) void scan_bwd_kernel(const BwdParams p)
 {
     typedef Work<T, NW, NL> W;
     constexpr int NT = W::NT, NP = W::NP, PASS = W::PASS;
-    constexpr int RED = SCAN_TILE + 4;                 // padded row of the sums over channels
+    constexpr int LPC = NW, NB = NL / 4;               // lanes per channel, groups of 4 states per lane
     __shared__ __align__(16) typename W::Lds lds;
-    __shared__ __align__(16) float part[NW][3][BWD_ROWS][SCAN_TILE];   // o, du, sum_n A w by wave
-    __shared__ __align__(16) float red[NW][8][RED];
-    __shared__ __align__(16) float bcout[BWD_ROWS][2 * NP];
+    __shared__ __align__(16) float part[4][BWD_ROWS][SCAN_TILE];       // o, du, sum_n A w, (unused)
+    __shared__ __align__(16) float bcw[NW][BWD_ROWS][2 * NP];          // dB and dC of the wave's channels
     W w(p);
     if (!w.live) return;
-    const int lane = w.lane, d = w.d, n0 = w.n0;
+    const int lane = w.lane, ng = lane % LPC;
+    const int chn = w.wave * (64 / LPC) + lane / LPC;  // the lane's channel in the tile
+    const int d = w.ch.d0 + chn, n0 = 4 * ng;          // states n0 + 4 LPC k + j
+    const bool own = chn < w.ch.count;
 
     float a2[NL], G[NL], dA[NL], enter[NL];
     // the gradient that reaches the piece's last state, and the state that enters it (of a
     // sequence's first piece the kept states already have it)
 #pragma unroll
-    for (int j = 0; j < NL; ++j) {
-        const bool live = w.own && n0 + j < p.N;
-        a2[j] = live ? p.A[(size_t)d * p.N + n0 + j] * LOG2E : 0.0f;
-        G[j] = live && p.dh_final ? p.dh_final[((size_t)w.b * p.D + d) * p.N + n0 + j] : 0.0f;
-        dA[j] = enter[j] = 0.0f;
+    for (int i = 0; i < NL; ++i) {
+        const int n = n0 + i / 4 * 4 * LPC + i % 4;
+        const bool live = own && n < p.N;
+        a2[i] = live ? p.A[(size_t)d * p.N + n] * LOG2E : 0.0f;
+        G[i] = live && p.dh_final ? p.dh_final[((size_t)w.b * p.D + d) * p.N + n] : 0.0f;
+        dA[i] = enter[i] = 0.0f;
     }
-    if (CUT && w.own) {
+    if (CUT && own) {
 #pragma unroll 4
         for (int e = w.number - w.c; e < w.number; ++e) {
             const float sum = p.piece_s[(size_t)e * p.D + d];
 #pragma unroll
-            for (int j = 0; j < NL; ++j)
-                enter[j] = fmaf(__builtin_amdgcn_exp2f(a2[j] * sum), enter[j], p.piece_h[((size_t)e * NP + n0 + j) * p.D + d]);
+            for (int i = 0; i < NL; ++i)
+                enter[i] = fmaf(__builtin_amdgcn_exp2f(a2[i] * sum), enter[i],
+                                p.piece_h[((size_t)e * NP + n0 + i / 4 * 4 * LPC + i % 4) * p.D + d]);
         }
 #pragma unroll 4
         for (int e = w.number - w.c + (w.sq.n - 1) / p.pieces.length; e > w.number; --e) {
             const float sum = p.piece_s[(size_t)e * p.D + d];
 #pragma unroll
-            for (int j = 0; j < NL; ++j)
-                G[j] = fmaf(__builtin_amdgcn_exp2f(a2[j] * sum), G[j], p.piece_g[((size_t)e * NP + n0 + j) * p.D + d]);
+            for (int i = 0; i < NL; ++i)
+                G[i] = fmaf(__builtin_amdgcn_exp2f(a2[i] * sum), G[i],
+                            p.piece_g[((size_t)e * NP + n0 + i / 4 * 4 * LPC + i % 4) * p.D + d]);
         }
     }
 
@@ -301,66 +338,80 @@ __global__ __launch_bounds__(64 * NW, 2) void scan_bwd_kernel(const BwdParams p)
     const int back = w.t_begin + (w.t_end - w.t_begin - 1) / BWD_ROWS * BWD_ROWS;
     if (w.t_begin < w.t_end) w.template load<true>(back);
     for (int t0 = back; t0 >= w.t_begin && w.t_begin < w.t_end; t0 -= BWD_ROWS) {
-        // the state in front of the tile
-        float h0[NL];
-        const size_t slot = w.slot + t0 / BWD_ROWS;
-        const float since = CUT && w.c > 0 && w.own ? p.before[slot * p.D + d] : 0.0f;
-#pragma unroll
-        for (int j = 0; j < NL; ++j) h0[j] = w.own ? p.state[(slot * NP + n0 + j) * p.D + d] : 0.0f;
         w.template put<true>(lds, t0);
         __syncthreads();
         if (t0 > w.t_begin) w.template load<true>(t0 - BWD_ROWS);
-        for_each<NL / 4>([&](auto qc) {                // four states at a time
+#pragma unroll 1
+        for (int half = BWD_ROWS - KEEP; half >= 0; half -= KEEP)
+        for_each<NB>([&](auto qc) {                    // KEEP rows and four states at a time
             constexpr int q = 4 * qc;
-            float h[BWD_ROWS + 1][4], a[BWD_ROWS][4];
+            const int n = n0 + q * LPC;
+            float h[KEEP + 1][4], a[KEEP][4];
+            // the state in front of the rows (rows past the end start from any)
+            const size_t slot = w.slot + min(t0 + half, w.t_end - 1) / KEEP;
+            const float since = CUT && w.c > 0 && own ? p.before[slot * p.D + d] : 0.0f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                h[0][j] = CUT ? fmaf(__builtin_amdgcn_exp2f(a2[q + j] * since), enter[q + j], h0[q + j]) : h0[q + j];
-#pragma unroll
-            for (int t = 0; t < BWD_ROWS; ++t) {
-                const float2 su = lds.su[t][lane];
-                const float2 bcv = lds.bc[t][n0 + (lane & (NL - 1))];
-                float o = 0.0f;
-                for_each<4>([&](auto jc) {
-                    constexpr int j = jc;
-                    a[t][j] = __builtin_amdgcn_exp2f(su.x * a2[q + j]);
-                    h[t + 1][j] = fmaf(a[t][j], h[t][j], row_broadcast<q + j>(bcv.x) * su.y);
-                    o = fmaf(row_broadcast<q + j>(bcv.y), h[t + 1][j], o);
-                });
-                part[w.wave][0][t][lane] = q == 0 ? o : part[w.wave][0][t][lane] + o;
+            for (int j = 0; j < 4; ++j) {
+                h[0][j] = own ? p.state[(slot * NP + n + j) * p.D + d] : 0.0f;
+                if (CUT) h[0][j] = fmaf(__builtin_amdgcn_exp2f(a2[q + j] * since), enter[q + j], h[0][j]);
             }
 #pragma unroll
-            for (int t = BWD_ROWS - 1; t >= 0; --t) {
-                const float2 su = lds.su[t][lane];
-                const float ds = lds.ds[t][lane];
-                const float2 bcv = lds.bc[t][n0 + (lane & (NL - 1))];
-                float du = 0.0f, aw = 0.0f;
-                for_each<4>([&](auto jc) {
-                    constexpr int j = jc;
-                    const float g = fmaf(row_broadcast<q + j>(bcv.y), ds, G[q + j]);
-                    du = fmaf(row_broadcast<q + j>(bcv.x), g, du);
+            for (int t = 0; t < KEEP; ++t) {
+                const float2 su = lds.su[half + t][chn];
+                const f32x4 bv = *reinterpret_cast<const f32x4*>(&lds.bs[half + t][n]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    a[t][j] = __builtin_amdgcn_exp2f(su.x * a2[q + j]);
+                    h[t + 1][j] = fmaf(a[t][j], h[t][j], bv[j] * su.y);
+                }
+            }
+#pragma unroll
+            for (int t = KEEP - 1; t >= 0; --t) {
+                const float2 su = lds.su[half + t][chn];
+                const float ds = lds.ds[half + t][chn];
+                const f32x4 bv = *reinterpret_cast<const f32x4*>(&lds.bs[half + t][n]);
+                const f32x4 cv = *reinterpret_cast<const f32x4*>(&lds.cs[half + t][n]);
+                float o = 0.0f, du = 0.0f, aw = 0.0f, v[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float g = fmaf(cv[j], ds, G[q + j]);
                     const float gw = g * (a[t][j] * h[t][j]);
-                    aw = fmaf(a2[q + j], gw, aw);
+                    o = j == 0 ? cv[0] * h[t + 1][0] : fmaf(cv[j], h[t + 1][j], o);
+                    du = j == 0 ? bv[0] * g : fmaf(bv[j], g, du);
+                    aw = j == 0 ? a2[q] * gw : fmaf(a2[q + j], gw, aw);
                     dA[q + j] = fmaf(su.x, gw, dA[q + j]);
                     G[q + j] = a[t][j] * g;
-                    red[w.wave][j][lane] = g * su.y;
-                    red[w.wave][4 + j][lane] = ds * h[t + 1][j];
-                });
-                part[w.wave][1][t][lane] = q == 0 ? du : part[w.wave][1][t][lane] + du;
-                part[w.wave][2][t][lane] = q == 0 ? aw : part[w.wave][2][t][lane] + aw;
-                // 8 sums over 64 channels (dB, dC; 4 states): 8 lanes a sum
-                __builtin_amdgcn_wave_barrier();
-                const float* at = &red[w.wave][lane >> 3][(lane & 7) * 8];
-                const f32x4 s4 = *reinterpret_cast<const f32x4*>(at) + *reinterpret_cast<const f32x4*>(at + 4);
-                float s1 = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                s1 += __shfl_xor(s1, 1, 64);
-                s1 += __shfl_xor(s1, 2, 64);
-                s1 += __shfl_xor(s1, 4, 64);
-                if ((lane & 7) == 0) {
-                    const int k = lane >> 3;           // dB or dC, state
-                    bcout[t][(k >> 2) * NP + n0 + q + (k & 3)] = s1;
+                    v[j] = g * su.y;
+                    v[4 + j] = ds * h[t + 1][j];
                 }
-                __builtin_amdgcn_wave_barrier();
+                // over the channel's states; lane ng of a channel stores the ng-th sum
+                if (LPC > 1) { o = add_xor<1>(o); du = add_xor<1>(du); aw = add_xor<1>(aw); }
+                if (LPC > 2) { o = add_xor<2>(o); du = add_xor<2>(du); aw = add_xor<2>(aw); }
+                float* to = &part[0][half + t][chn];
+                constexpr int PLANE = BWD_ROWS * SCAN_TILE;
+                auto put = [&](int plane, float x) { to[plane * PLANE] = q == 0 ? x : to[plane * PLANE] + x; };
+                if (LPC == 4) {
+                    put(ng, ng == 0 ? o : ng == 1 ? du : aw);
+                } else if (LPC == 2) {
+                    put(ng, ng == 0 ? o : du);
+                    put(2 + ng, aw);
+                } else {
+                    put(0, o);
+                    put(1, du);
+                    put(2, aw);
+                }
+                // over the wave's channels: value 4 bit5 + 2 bit4 + k of lane's r[k]
+                float r[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    r[k] = add_rows(add_halves(v[k], v[4 + k]), add_halves(v[2 + k], v[6 + k]));
+                    r[k] = add_ror<4>(add_ror<8>(r[k]));
+                    if (LPC < 4) r[k] = add_ror<2>(r[k]);
+                    if (LPC < 2) r[k] = add_ror<1>(r[k]);
+                }
+                const int k = lane >> 2 & 1, j = 2 * (lane >> 4 & 1) + k;
+                // (lanes of one sum hold the same bits and store them to one address: no branch)
+                bcw[w.wave][half + t][(lane >> 5) * NP + n + j] = k ? r[1] : r[0];
             }
         });
         __syncthreads();
@@ -370,11 +421,8 @@ __global__ __launch_bounds__(64 * NW, 2) void scan_bwd_kernel(const BwdParams p)
             const int n = t < w.t_end ? w.ch.count - w.c4 : 0;
             f32x4 sum[3];                              // o, du, sum_n A w
 #pragma unroll
-            for (int q = 0; q < 3; ++q) {
-                sum[q] = *reinterpret_cast<const f32x4*>(&part[0][q][r][w.c4]);
-#pragma unroll
-                for (int k = 1; k < NW; ++k) sum[q] += *reinterpret_cast<const f32x4*>(&part[k][q][r][w.c4]);
-            }
+            for (int q = 0; q < 3; ++q)
+                sum[q] = *reinterpret_cast<const f32x4*>(&part[q][r][w.c4]);
             const f32x4 sa = *reinterpret_cast<const f32x4*>(&lds.su[r][w.c4]);
             const f32x4 sb = *reinterpret_cast<const f32x4*>(&lds.su[r][w.c4 + 2]);
             const f32x4 ds = *reinterpret_cast<const f32x4*>(&lds.ds[r][w.c4]);
@@ -409,33 +457,37 @@ __global__ __launch_bounds__(64 * NW, 2) void scan_bwd_kernel(const BwdParams p)
         }
         for (int at = w.tid; at < BWD_ROWS * 2 * NP; at += NT) {
             const int r = at / (2 * NP);
-            if (t0 + r < w.t_end) bcp[(size_t)(t0 + r) * (2 * NP) + at % (2 * NP)] = bcout[r][at % (2 * NP)];
+            float v = bcw[0][r][at % (2 * NP)];
+#pragma unroll
+            for (int k = 1; k < NW; ++k) v += bcw[k][r][at % (2 * NP)];
+            if (t0 + r < w.t_end) bcp[(size_t)(t0 + r) * (2 * NP) + at % (2 * NP)] = v;
         }
         __syncthreads();
     }
 
     // the piece's sums; those of dskip and dbias lie with the NT / 16 threads of a channel group
     float* so = p.sums + (size_t)w.number * (NP + 2) * p.D;
-    if (w.own) {
+    if (own) {
 #pragma unroll
-        for (int j = 0; j < NL; ++j) {
-            so[(size_t)(n0 + j) * p.D + d] = dA[j];
-            if (w.c == 0 && p.dh_init && n0 + j < p.N) p.dh_init[((size_t)w.b * p.D + d) * p.N + n0 + j] = G[j];
+        for (int i = 0; i < NL; ++i) {
+            const int n = n0 + i / 4 * 4 * LPC + i % 4;
+            so[(size_t)n * p.D + d] = dA[i];
+            if (w.c == 0 && p.dh_init && n < p.N) p.dh_init[((size_t)w.b * p.D + d) * p.N + n] = G[i];
         }
     }
-    float* sm = &part[0][0][0][0];
+    float* sm = &part[0][0][0];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         sm[w.r0 * SCAN_TILE + w.c4 + e] = dskip[e];
         sm[(NT / 16 + w.r0) * SCAN_TILE + w.c4 + e] = dbias[e];
     }
     __syncthreads();
-    if (w.tid < SCAN_TILE && w.own) {
+    if (w.tid < SCAN_TILE && w.own) {                  // (here a thread is its lane's channel again)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             float s = 0.0f;
             for (int r = 0; r < NT / 16; ++r) s += sm[(k * (NT / 16) + r) * SCAN_TILE + lane];
-            so[(size_t)(NP + k) * p.D + d] = s;
+            so[(size_t)(NP + k) * p.D + w.d] = s;
         }
     }
 }
@@ -483,11 +535,30 @@ __global__ __launch_bounds__(256) void scan_bwd_bc_kernel(const BwdParams p, int
     out[g * p.N + n] = from_f32<T>(s);
 }
 
+// Rows per piece.  Cutting costs the R and the sums of the first kernel (about a tenth of the
+// whole), and pays where whole sequences would leave the 512 places (two workgroups to a
+// compute unit) unfilled: (sequences, rows, channels) = (16, 1024, 2048), 512 workgroups, took
+// 646 us whole and 719 us in four pieces; (4, 2048, 4096), 256 workgroups, 941 us whole, 775, 743
+// and 732 us in 2, 4 and 8; (8, 2048, 1536) 917 us whole, 748, 594, 629 and 555 us in 2, 4, 6 and
+// 8.  The 6 lose because their workgroups fill the places 2.25 times: so the number is taken that
+// makes rounds * rows the least, with 24 rows for a piece's start, and among numbers within a
+// twentieth of that the largest.
+constexpr int PLACES = 512, WHOLE_FROM = 448, MOST_WORKGROUPS = 2048, SHORTEST_PIECE = 64, START_ROWS = 24;
 int piece_rows(int S, int rows, int D, int G) {
+    // packed sequences count by the rows that there are
     const long long groups = (long long)scan_tiles(D, G) * ((rows + S - 1) / S);
     const int whole = (S + BWD_ROWS - 1) / BWD_ROWS * BWD_ROWS;
-    int n = 1; if (getenv("SCANBK")) n = atoi(getenv("SCANBK"));
-    return (((S + n - 1) / n + 15) / 16 * 16);
+    if (groups >= WHOLE_FROM || whole <= SHORTEST_PIECE) return whole;
+    auto length = [&](int n) { return (int)(((S + n - 1) / n + BWD_ROWS - 1) / BWD_ROWS * BWD_ROWS); };
+    auto cost = [&](int n) { return (groups * n + PLACES - 1) / PLACES * (length(n) + START_ROWS); };
+    long long least = cost(1);
+    const int most = (int)(MOST_WORKGROUPS / groups);
+    for (int n = 2; n <= most && length(n) >= SHORTEST_PIECE; ++n)
+        if (cost(n) < least) least = cost(n);
+    int best = 1;
+    for (int n = 2; n <= most && length(n) >= SHORTEST_PIECE; ++n)
+        if (20 * cost(n) <= 21 * least) best = n;
+    return length(best);
 }
 
 struct BwdPlan {
@@ -504,7 +575,7 @@ BwdPlan plan(const int* seq_start, int B, int S, int rows, int D, int G, int N) 
     auto take = [&](size_t n) { const size_t o = at; at += (n + 63) / 64 * 64; return o; };
     // as many tiles of rows and pieces as packed sequences may need (also where they are not
     // packed: a workspace's size does not depend on seq_start)
-    const size_t slots = (size_t)rows / BWD_ROWS + B, parts = (size_t)rows / f.pieces.length + B;
+    const size_t slots = (size_t)rows / KEEP + B, parts = (size_t)rows / f.pieces.length + B;
     f.state = take(slots * NP * D);
     f.bc = take((size_t)scan_tiles(D, G) * rows * 2 * NP);
     f.sums = take(parts * (NP + 2) * D);
