@@ -525,7 +525,7 @@ mlstm_status ssm_conv_step(const void *x, long long x_stride, const float *weigh
  *   grad_state_init [B,width-1,D] dtype, or NULL (not wanted)
  *   workspace: ssm_conv_bwd_workspace_bytes(...) bytes, 4-byte aligned
  */
-size_t ssm_conv_bwd_workspace_bytes(int B, int S, int D, int width);
+size_t ssm_conv_bwd_workspace_bytes(int B, int rows, int D, int width);
 mlstm_status ssm_conv_bwd(const void *x, long long x_stride, const float *weight, const float *bias,
                           const int *seq_start, const void *state_init,
                           const void *dy, long long dy_stride, const void *dstate_final,

@@ -859,8 +859,8 @@ def ssm_conv_step(x, weight, state, bias=None, act: int = SSM_ACT_SWISH, y_out=N
     return y_out
 
 
-def ssm_conv_bwd_workspace_bytes(B: int, S: int, D: int, width: int) -> int:
-    return int(load_library().ssm_conv_bwd_workspace_bytes(B, S, D, width))
+def ssm_conv_bwd_workspace_bytes(B: int, rows: int, D: int, width: int) -> int:
+    return int(load_library().ssm_conv_bwd_workspace_bytes(B, rows, D, width))
 
 
 def ssm_conv_bwd(x, weight, dy, bias=None, act: int = SSM_ACT_SWISH, state_init=None, seq_start=None, max_len=None,
@@ -888,7 +888,7 @@ def ssm_conv_bwd(x, weight, dy, bias=None, act: int = SSM_ACT_SWISH, state_init=
     grad_bias = None if bias is None else torch.empty((D,), dtype=torch.float32, device=dev)
     grad_state = None if state_init is None else torch.empty((B, W - 1, D), dtype=x.dtype, device=dev)
     owned += [grad_weight, grad_bias, grad_state]
-    ws, ws_bytes = _workspace(workspace, ssm_conv_bwd_workspace_bytes(B, S, D, W), dev, owned)
+    ws, ws_bytes = _workspace(workspace, ssm_conv_bwd_workspace_bytes(B, rows, D, W), dev, owned)
     _keep_for_stream(stream, dev, owned)
     _launch("ssm_conv_bwd", dev, x.data_ptr(), _row_stride(x, "x"), weight.data_ptr(), _ptr(bias), _ptr(seq_start),
             _ptr(state_init), dy.data_ptr(), _row_stride(dy, "dy"), _ptr(dstate_final), B, S, rows, D, W, int(act), dt,

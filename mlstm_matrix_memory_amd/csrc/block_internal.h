@@ -210,7 +210,7 @@ struct ConvArgs {
 };
 hipError_t launch_conv_fwd(const ConvArgs& a);
 hipError_t launch_conv_step(const ConvArgs& a);
-size_t conv_bwd_workspace_bytes(int B, int S, int D, int width);
+size_t conv_bwd_workspace_bytes(int B, int rows, int D, int width);
 hipError_t launch_conv_bwd(const ConvArgs& a);
 
 struct ScanArgs {

@@ -70,9 +70,10 @@ mlstm_status ssm_conv_step(const void* x, long long x_stride, const float* weigh
     return launched(mlstm::launch_conv_step(a));
 }
 
-size_t ssm_conv_bwd_workspace_bytes(int B, int S, int D, int width) {
-    if (B < 1 || S < 1 || D < 1 || B > MAX_SEQUENCES || check_conv(width, SSM_ACT_NONE, MLSTM_F32) != MLSTM_OK) return 0;
-    return mlstm::conv_bwd_workspace_bytes(B, S, D, width);
+size_t ssm_conv_bwd_workspace_bytes(int B, int rows, int D, int width) {
+    if (B < 1 || rows < 1 || D < 1 || B > MAX_SEQUENCES || rows > MAX_ROWS) return 0;
+    if (check_conv(width, SSM_ACT_NONE, MLSTM_F32) != MLSTM_OK) return 0;
+    return mlstm::conv_bwd_workspace_bytes(B, rows, D, width);
 }
 
 mlstm_status ssm_conv_bwd(const void* x, long long x_stride, const float* weight, const float* bias,
@@ -83,7 +84,7 @@ mlstm_status ssm_conv_bwd(const void* x, long long x_stride, const float* weight
                           void* grad_state_init, void* ws, size_t workspace_bytes, void* stream) {
     MLSTM_TRY(batch(B, S, rows, D, seq_start));
     MLSTM_TRY(check_conv(width, act, dt));
-    const size_t need = mlstm::conv_bwd_workspace_bytes(B, S, D, width);
+    const size_t need = mlstm::conv_bwd_workspace_bytes(B, rows, D, width);
     MLSTM_TRY(workspace(ws, workspace_bytes, need, 4));
     if (!bias && grad_bias) return fail(MLSTM_ERR_INVALID_ARG, "grad_bias is given without bias");
     const size_t el = elem(dt), st = (size_t)B * (width - 1) * D;

@@ -6,16 +6,25 @@
 // Backward, with dp_t = dy_t act'(p_t) (0 outside the sequence):
 //   dx_t = sum_j w_j dp_{t+W-1-j},  dw_j = sum_t dp_t x_{t-W+1+j},  dbias = sum_t dp_t
 //
-// A thread owns 8 neighbouring channels (one 16-byte access of a bf16 row) and walks
-// a run of rows with the last W - 1 inputs in registers, so that each input is read
-// once, but for the W - 1 rows at a run's start.  Threads are numbered through
-// channels first: a wave's accesses are contiguous for any D.  Bound by HBM.
+// A thread owns 8 neighbouring channels (one 16-byte access of a bf16 row) and a run of
+// rows, fully unrolled: all of a run's loads are in flight together, and the W - 1 rows that
+// neighbouring runs share come from the cache.  A workgroup is 32 threads of channels by
+// 8 runs.  Bound by HBM.
+//
+// Where D is no multiple of 8 the last thread of a row takes the row's last 8 channels,
+// some of them its neighbour's too: both compute and store the same values, and the
+// wave has one path.  (With guarded accesses for the last channels it ran both paths one
+// after the other: the backward at D = 1537 took 59 us against 33 us at 1536.)
+#include <type_traits>
+
 #include "block_internal.h"
 
 namespace mlstm {
 namespace {
 
 constexpr int CONV_THREADS = 256;
+constexpr int CONV_LANES = 32;                         // threads along the channels
+constexpr int CONV_RUNS = CONV_THREADS / CONV_LANES;   // runs of a workgroup
 
 // rows before the first of a sequence: row -m (1 <= m < W) is row W - 1 - m of its state
 template <typename T, int W>
@@ -27,60 +36,98 @@ __device__ __forceinline__ Raw8<T> load_input(const T* x, long long stride, cons
     return z;
 }
 
-template <typename T, int W, bool ACT>
+// eight channels' taps w[j][e] and bias
+template <int W>
+__device__ __forceinline__ void load_taps(const float* weight, const float* bias, int c, int n, float (&w)[W][8],
+                                          float (&bs)[8]) {
+    if (n >= 8) {
+        float v[8 * W];
+#pragma unroll
+        for (int k = 0; k < 2 * W; ++k)
+            *reinterpret_cast<f32x4*>(v + 4 * k) = *reinterpret_cast<const f32x4_u*>(weight + (size_t)c * W + 4 * k);
+        const Raw8<float> bv = load_row8(bias ? bias + c : weight, bias ? 8 : 0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][e] = v[e * W + j];
+            bs[e] = bv.get(e);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][e] = e < n ? weight[(size_t)(c + e) * W + j] : 0.0f;
+            bs[e] = bias && e < n ? bias[c + e] : 0.0f;
+        }
+    }
+}
+
+template <typename T, int W, bool ACT, int RUN>
 __global__ __launch_bounds__(CONV_THREADS) void conv_fwd_kernel(
     const T* __restrict__ x, long long x_stride, const float* __restrict__ weight, const float* __restrict__ bias,
-    const int* __restrict__ seq_start, const T* __restrict__ state_init, int S, int rows, int D, int run,
-    T* __restrict__ y, long long y_stride, T* __restrict__ state_final)
+    const T* __restrict__ state_init, const Pieces pieces, int D, T* __restrict__ y, long long y_stride,
+    T* __restrict__ state_final)
 {
-    const int groups = (D + 7) / 8;
-    const long long id = (long long)blockIdx.x * CONV_THREADS + threadIdx.x;
-    const int c = (int)(id % groups) * 8;
-    const long long t_first = id / groups * run;
-    if (t_first >= S) return;
-    const int b = blockIdx.y;
-    const RowRange sq = sequence_rows(seq_start, b, S, rows);
-    const int n = D - c;
+    const int blocks = ((D + 7) / 8 + CONV_LANES - 1) / CONV_LANES;
+    int c = ((blockIdx.x % blocks) * CONV_LANES + threadIdx.x % CONV_LANES) * 8;
+    if (c >= D) return;
+    if (D >= 8) c = min(c, D - 8);
+    const int n = D - c;                               // below 8 only where D is
+    const Pieces::At at = pieces.at(blockIdx.x / blocks);
+    const RowRange sq = pieces.sequence(at.b);
+    const long long first = (long long)at.c * pieces.length + threadIdx.x / CONV_LANES * RUN;
+    if (first >= sq.n && first > 0) return;
+    const int t0 = (int)first;
     const T* xs = x + sq.lo * x_stride + c;
-    const T* st = state_init ? state_init + (size_t)b * (W - 1) * D + c : nullptr;
-    const int t0 = (int)t_first, t1 = min(t0 + run, sq.n);
+    const T* st = state_init ? state_init + (size_t)at.b * (W - 1) * D + c : nullptr;
     if (t0 == 0 && state_final) {
-        T* sf = state_final + (size_t)b * (W - 1) * D + c;
+        T* sf = state_final + (size_t)at.b * (W - 1) * D + c;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
             store_row8(sf + (size_t)j * D, load_input<T, W>(xs, x_stride, st, D, sq.n - (W - 1) + j, n), n);
     }
-    if (t0 >= t1) return;
-    float w[W][8], bs[8], past[W - 1][8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j][e] = e < n ? weight[(size_t)(c + e) * W + j] : 0.0f;
-        bs[e] = bias && e < n ? bias[c + e] : 0.0f;
-    }
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        const Raw8<T> v = load_input<T, W>(xs, x_stride, st, D, t0 - (W - 1) + j, n);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) past[j][e] = v.get(e);
-    }
+    if (t0 >= sq.n) return;
     T* ys = y + sq.lo * y_stride + c;
-    for (int t = t0; t < t1; ++t) {
-        const Raw8<T> v = load_row8(xs + t * x_stride, n);
-        Raw8<T> o;
+    auto run = [&](auto full) {
+        constexpr bool FULL = full;                    // all eight channels
+        Raw8<T> in[RUN + W - 1];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float p = bs[e];
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) p = fmaf(w[j][e], past[j][e], p);
-            p = fmaf(w[W - 1][e], v.get(e), p);
-            o.set(e, ACT ? p * sigmoid_hw(p) : p);
-#pragma unroll
-            for (int j = 0; j + 1 < W - 1; ++j) past[j][e] = past[j + 1][e];
-            past[W - 2][e] = v.get(e);
+        for (int i = 0; i < RUN; ++i) {                // rows past the end: the last, not stored
+            const T* row = xs + (long long)min(t0 + i, sq.n - 1) * x_stride;
+            if (FULL) in[W - 1 + i].load(row);
+            else in[W - 1 + i] = load_row8(row, n);
         }
-        store_row8(ys + t * y_stride, o, n);
-    }
+        if (t0 > 0) {
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) {
+                const T* row = xs + (long long)(t0 - (W - 1) + j) * x_stride;
+                if (FULL) in[j].load(row);
+                else in[j] = load_row8(row, n);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) in[j] = load_input<T, W>(xs, x_stride, st, D, j - (W - 1), n);
+        }
+        float w[W][8], bs[8];
+        load_taps<W>(weight, bias, c, n, w, bs);
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) {
+            Raw8<T> o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float p = bs[e];
+#pragma unroll
+                for (int j = 0; j < W; ++j) p = fmaf(w[j][e], in[i + j].get(e), p);
+                o.set(e, ACT ? p * sigmoid_hw(p) : p);
+            }
+            if (t0 + i < sq.n) {
+                if (FULL) o.store(ys + (long long)(t0 + i) * y_stride);
+                else store_row8(ys + (long long)(t0 + i) * y_stride, o, n);
+            }
+        }
+    };
+    if (n >= 8) run(std::true_type());
+    else run(std::false_type());
 }
 
 template <typename T, int W, bool ACT>
@@ -98,12 +145,14 @@ __global__ __launch_bounds__(64) void conv_step_kernel(
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) in[j] = load_row8(st + (size_t)j * D, n);
     in[W - 1] = load_row8(x + b * x_stride + c, n);
+    float w[W][8], bs[8];
+    load_taps<W>(weight, bias, c, n, w, bs);
     Raw8<T> o;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        float p = bias && e < n ? bias[c + e] : 0.0f;
+        float p = bs[e];
 #pragma unroll
-        for (int j = 0; j < W; ++j) p = fmaf(e < n ? weight[(size_t)(c + e) * W + j] : 0.0f, in[j].get(e), p);
+        for (int j = 0; j < W; ++j) p = fmaf(w[j][e], in[j].get(e), p);
         o.set(e, ACT ? p * sigmoid_hw(p) : p);
     }
 #pragma unroll
@@ -111,112 +160,165 @@ __global__ __launch_bounds__(64) void conv_step_kernel(
     store_row8(y + b * y_stride + c, o, n);
 }
 
-// A run of rows [t0, t1): its dp give dw and dbias; dx of row t needs dp up to row
-// t + W - 1, so the run reads W - 1 rows past its end.  The first run of a sequence
-// also emits the gradient of the rows before it (its initial state).
+// A run of BWD_RUN rows: its dp give dw and dbias; dx of row t needs dp up to row t + W - 1, so
+// a run reads W - 1 rows past its end.  The first run of a sequence also emits the gradient of
+// the rows before it (its initial state).  A thread owns 4 channels here: taps, sums and
+// windows of 8 took 396 registers, one wave to a SIMD.  The workgroup, 64 threads of channels
+// by 4 runs, adds its runs' dw and dbias in LDS and writes one part of them.
+constexpr int BWD_RUN = 29;                            // with W = 4, 8 blocks of 4 rows
+constexpr int BWD_RUNS = CONV_THREADS / 64;
 template <typename T, int W, bool ACT>
 __global__ __launch_bounds__(CONV_THREADS) void conv_bwd_kernel(
     const T* __restrict__ x, long long x_stride, const float* __restrict__ weight, const float* __restrict__ bias,
-    const int* __restrict__ seq_start, const T* __restrict__ state_init,
-    const T* __restrict__ dy, long long dy_stride, const T* __restrict__ dstate_final,
-    int S, int rows, int D, int run, T* __restrict__ dx, long long dx_stride, T* __restrict__ grad_state,
-    float* __restrict__ parts)
+    const T* __restrict__ state_init, const T* __restrict__ dy, long long dy_stride,
+    const T* __restrict__ dstate_final, const Pieces pieces, int D, T* __restrict__ dx, long long dx_stride,
+    T* __restrict__ grad_state, float* __restrict__ parts)
 {
-    const int groups = (D + 7) / 8;
-    const long long id = (long long)blockIdx.x * CONV_THREADS + threadIdx.x;
-    const int c = (int)(id % groups) * 8;
-    const long long chunk = id / groups, t_first = chunk * run;
-    if (t_first >= S) return;
-    const int b = blockIdx.y;
-    const RowRange sq = sequence_rows(seq_start, b, S, rows);
-    const int n = D - c;
-    const T* xs = x + sq.lo * x_stride + c;
-    const T* gs = dy + sq.lo * dy_stride + c;
-    const T* st = state_init ? state_init + (size_t)b * (W - 1) * D + c : nullptr;
-    const T* df = dstate_final ? dstate_final + (size_t)b * (W - 1) * D + c : nullptr;
-    T* dxs = dx + sq.lo * dx_stride + c;
-    T* gst = grad_state ? grad_state + (size_t)b * (W - 1) * D + c : nullptr;
-    const int t0 = (int)t_first, t1 = min(t0 + run, sq.n);
-    float w[W][8], bs[8], past[W - 1][8], dp[W][8], dw[W][8], db[8];
+    __shared__ __align__(16) float red[BWD_RUNS][W + 1][256];
+    const int blocks = (D + 255) / 256;
+    const int lane = threadIdx.x & 63, turn = threadIdx.x >> 6;
+    const int c0 = (blockIdx.x % blocks) * 256, own = D - (c0 + lane * 4);
+    const int c = D >= 4 ? min(c0 + lane * 4, D - 4) : c0 + lane * 4;
+    const int n = own > 0 ? D - c : 0;                 // below 4 only where D is, or no channel is left
+    const int number = blockIdx.x / blocks;
+    const Pieces::At at = pieces.at(number);
+    const RowRange sq = pieces.sequence(at.b);
+    const long long piece = (long long)at.c * pieces.length;
+    const bool live = piece < sq.n || at.c == 0;       // (of others the part is zero)
+    const long long first = piece + turn * BWD_RUN;
+    float dw[W][4], db[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 4; ++e) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            w[j][e] = e < n ? weight[(size_t)(c + e) * W + j] : 0.0f;
-            dw[j][e] = 0.0f;
-            dp[j][e] = 0.0f;
-        }
-        bs[e] = bias && e < n ? bias[c + e] : 0.0f;
+        for (int j = 0; j < W; ++j) dw[j][e] = 0.0f;
         db[e] = 0.0f;
     }
+    if (live && n > 0 && (first < sq.n || first == 0)) {
+        const int t0 = (int)first, t1 = min(t0 + BWD_RUN, sq.n);
+        const T* xs = x + sq.lo * x_stride + c;
+        const T* gs = dy + sq.lo * dy_stride + c;
+        const T* st = state_init ? state_init + (size_t)at.b * (W - 1) * D + c : nullptr;
+        const T* df = dstate_final ? dstate_final + (size_t)at.b * (W - 1) * D + c : nullptr;
+        T* dxs = dx + sq.lo * dx_stride + c;
+        T* gst = grad_state ? grad_state + (size_t)at.b * (W - 1) * D + c : nullptr;
+        float w[W][4], bs[4], past[W - 1][4], dp[W][4];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        const Raw8<T> v = load_input<T, W>(xs, x_stride, st, D, t0 - (W - 1) + j, n);
+        for (int e = 0; e < 4; ++e) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) past[j][e] = v.get(e);
-    }
-    // rows t1 .. t1 + W - 2 only complete the gradients of this run's rows
-    const int end = t0 < t1 || t0 == 0 ? max(t1, t0) + W - 1 : t0;
-    for (int t = t0; t < end; ++t) {
-        Raw8<T> v, g;
-        v.zero();
-        g.zero();
-        if (t < sq.n) {
-            v = load_row8(xs + t * x_stride, n);
-            g = load_row8(gs + t * dy_stride, n);
+            for (int j = 0; j < W; ++j) w[j][e] = e < n ? weight[(size_t)(c + e) * W + j] : 0.0f;
+            bs[e] = bias && e < n ? bias[c + e] : 0.0f;
         }
-        const int s = t - (W - 1);                       // the row whose gradient is complete now
-        const int held = s - (sq.n - (W - 1));           // its place in the final state, if >= 0
-        Raw8<T> more, o;
-        more.zero();
-        if (df && held >= 0 && held < W - 1) more = load_row8(df + (size_t)held * D, n);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float p = bs[e];
+        for (int j = 0; j < W - 1; ++j) {
+            const int t = t0 - (W - 1) + j;
+            Raw4<T> v;
+            if (t >= 0) v = load_row4(xs + (long long)t * x_stride, n);
+            else v = load_row4(st ? st + (size_t)(W - 1 + t) * D : xs, st ? n : 0);
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) p = fmaf(w[j][e], past[j][e], p);
-            p = fmaf(w[W - 1][e], v.get(e), p);
-            float d = g.get(e);
-            if (ACT) {
-                const float sg = sigmoid_hw(p);
-                d *= sg * (1.0f + p * (1.0f - sg));
-            }
-#pragma unroll
-            for (int j = 0; j + 1 < W; ++j) dp[j][e] = dp[j + 1][e];
-            dp[W - 1][e] = d;
-            if (t < t1) {
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) dw[j][e] = fmaf(d, past[j][e], dw[j][e]);
-                dw[W - 1][e] = fmaf(d, v.get(e), dw[W - 1][e]);
-                db[e] += d;
-            }
-            // dx_s = sum_j w_j dp_{s + W - 1 - j};  dp[i] holds row s + i
-            float a = more.get(e);
-#pragma unroll
-            for (int j = 0; j < W; ++j) a = fmaf(w[j][e], dp[W - 1 - j][e], a);
-            o.set(e, a);
-#pragma unroll
-            for (int j = 0; j + 1 < W - 1; ++j) past[j][e] = past[j + 1][e];
-            past[W - 2][e] = v.get(e);
+            for (int e = 0; e < 4; ++e) past[j][e] = v.get(e);
         }
-        if (s >= t0 && s < t1) store_row8(dxs + s * dx_stride, o, n);
-        if (s < 0 && gst) store_row8(gst + (size_t)(W - 1 + s) * D, o, n);
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dp[j][e] = 0.0f;
+        auto run = [&](auto full) {
+            constexpr bool FULL = full;                // all four channels, and rows to read
+            // blocks of BLOCK rows, the next block's loads in flight beside one's arithmetic
+            constexpr int BLOCK = 4;
+            Raw4<T> xv[BLOCK], gv[BLOCK], xn[BLOCK], gn[BLOCK];
+            auto load = [&](int t) {
+#pragma unroll
+                for (int i = 0; i < BLOCK; ++i) {
+                    if (FULL) {                        // rows past the end: the last, masked below
+                        const long long r = min(t + i, sq.n - 1);
+                        xn[i].load(xs + r * x_stride);
+                        gn[i].load(gs + r * dy_stride);
+                    } else {
+                        const int m = t + i < sq.n ? n : 0;
+                        xn[i] = load_row4(xs + (long long)(t + i) * x_stride, m);
+                        gn[i] = load_row4(gs + (long long)(t + i) * dy_stride, m);
+                    }
+                }
+            };
+            load(t0);
+            const int end = t1 + W - 1;                // rows from t1 on only complete gradients
+            for (int tb = t0; tb < end; tb += BLOCK) {
+#pragma unroll
+                for (int i = 0; i < BLOCK; ++i) {
+                    xv[i] = xn[i];
+                    gv[i] = gn[i];
+                }
+                load(tb + BLOCK);
+#pragma unroll
+                for (int i = 0; i < BLOCK; ++i) {
+                    const int t = tb + i;
+                    const int s = t - (W - 1);                   // the row whose gradient is complete now
+                    const int held = s - (sq.n - (W - 1));       // its place in the final state, if >= 0
+                    Raw4<T> more, o;
+                    more.zero();
+                    if (df && held >= 0 && held < W - 1) more = load_row4(df + (size_t)held * D, n);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float v = t < sq.n ? xv[i].get(e) : 0.0f;
+                        float p = bs[e];
+#pragma unroll
+                        for (int j = 0; j < W - 1; ++j) p = fmaf(w[j][e], past[j][e], p);
+                        p = fmaf(w[W - 1][e], v, p);
+                        float g = gv[i].get(e);
+                        if (ACT) {
+                            const float sg = sigmoid_hw(p);
+                            g *= sg * (1.0f + p * (1.0f - sg));
+                        }
+                        g = t < sq.n ? g : 0.0f;
+#pragma unroll
+                        for (int j = 0; j + 1 < W; ++j) dp[j][e] = dp[j + 1][e];
+                        dp[W - 1][e] = g;
+                        const float gw = t < t1 ? g : 0.0f;
+#pragma unroll
+                        for (int j = 0; j < W - 1; ++j) dw[j][e] = fmaf(gw, past[j][e], dw[j][e]);
+                        dw[W - 1][e] = fmaf(gw, v, dw[W - 1][e]);
+                        db[e] += gw;
+                        // dx_s = sum_j w_j dp_{s + W - 1 - j};  dp[i] holds row s + i
+                        float a = more.get(e);
+#pragma unroll
+                        for (int j = 0; j < W; ++j) a = fmaf(w[j][e], dp[W - 1 - j][e], a);
+                        o.set(e, a);
+#pragma unroll
+                        for (int j = 0; j + 1 < W - 1; ++j) past[j][e] = past[j + 1][e];
+                        past[W - 2][e] = v;
+                    }
+                    if (s >= t0 && s < t1) {
+                        if (FULL) o.store(dxs + (long long)s * dx_stride);
+                        else store_row4(dxs + (long long)s * dx_stride, o, n);
+                    }
+                    if (s < 0 && gst) store_row4(gst + (size_t)(W - 1 + s) * D, o, n);
+                }
+            }
+        };
+        if (n >= 4 && sq.n > 0) run(std::true_type());
+        else run(std::false_type());
     }
-    // parts [(b, run)][W + 1][D]
-    const long long runs = (S + run - 1) / run;
-    float* po = parts + (size_t)(b * runs + chunk) * (W + 1) * D + c;
+    // of the channels it shares with its neighbour a thread adds none
+    const int skip = own > 0 && own < 4 && D >= 4 ? 4 - own : 0;
+#pragma unroll
+    for (int j = 0; j <= W; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e >= skip) red[turn][j][lane * 4 + e - skip] = j < W ? dw[j < W ? j : 0][e] : db[e];
+    __syncthreads();
+    if (c0 + (int)threadIdx.x >= D) return;
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
-        Raw8<float> o;
+        float v = red[0][j][threadIdx.x];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o.set(e, j < W ? dw[j < W ? j : 0][e] : db[e]);
-        store_row8(po + (size_t)j * D, o, n);
+        for (int k = 1; k < BWD_RUNS; ++k) v += red[k][j][threadIdx.x];
+        parts[((size_t)number * (W + 1) + j) * D + c0 + threadIdx.x] = v;
     }
 }
 
 // dweight[d][j], dbias[d] = sums of the parts: 64 channels of one tap per workgroup
 template <int W>
-__global__ __launch_bounds__(1024) void conv_sum_kernel(const float* __restrict__ parts, long long n, int D,
+__global__ __launch_bounds__(1024) void conv_sum_kernel(const float* __restrict__ parts, int count, int D,
                                                         float* __restrict__ dw, float* __restrict__ db)
 {
     __shared__ float sm[16][64];
@@ -225,7 +327,7 @@ __global__ __launch_bounds__(1024) void conv_sum_kernel(const float* __restrict_
     float s = 0.0f;
     if (d < D)
 #pragma unroll 8
-        for (long long p = wave; p < n; p += 16) s += parts[((size_t)p * (W + 1) + j) * D + d];
+        for (int i = wave; i < count; i += 16) s += parts[((size_t)i * (W + 1) + j) * D + d];
     sm[wave][lane] = s;
     __syncthreads();
     if (wave == 0 && d < D) {
@@ -236,28 +338,22 @@ __global__ __launch_bounds__(1024) void conv_sum_kernel(const float* __restrict_
     }
 }
 
-// Rows per run of the forward: 16 where the sequence is long, fewer where that leaves
-// the chip's 1024 SIMDs without two waves each.
-int conv_run(int B, int S, int D, int longest) {
-    const long long groups = (D + 7) / 8;
-    int run = longest;
-    while (run > 4 && (long long)B * groups * ((S + run - 1) / run) < 131072) run >>= 1;
-    return run;
-}
-constexpr int CONV_FWD_RUN = 16;
-constexpr int CONV_BWD_RUN = 128;
+int conv_blocks(int D) { return ((D + 7) / 8 + CONV_LANES - 1) / CONV_LANES; }
 
-dim3 conv_grid(int B, int S, int D, int run) {
-    const long long threads = (long long)((D + 7) / 8) * ((S + run - 1) / run);
-    return dim3((unsigned)((threads + CONV_THREADS - 1) / CONV_THREADS), (unsigned)B);
+template <typename T, int W, bool ACT, int RUN>
+void fwd_run(const ConvArgs& a) {
+    const Pieces pieces = make_pieces(a.seq_start, a.B, a.S, a.rows, RUN * CONV_RUNS);
+    hipLaunchKernelGGL((conv_fwd_kernel<T, W, ACT, RUN>), dim3((unsigned)conv_blocks(a.D) * pieces.count()),
+                       dim3(CONV_THREADS), 0, a.stream, (const T*)a.x, a.x_stride, a.weight, a.bias,
+                       (const T*)a.state_init, pieces, a.D, (T*)a.y, a.y_stride, (T*)a.state_final);
 }
 
 template <typename T, int W, bool ACT>
 hipError_t fwd_t(const ConvArgs& a) {
-    const int run = conv_run(a.B, a.S, a.D, CONV_FWD_RUN);
-    hipLaunchKernelGGL((conv_fwd_kernel<T, W, ACT>), conv_grid(a.B, a.S, a.D, run), dim3(CONV_THREADS), 0, a.stream,
-                       (const T*)a.x, a.x_stride, a.weight, a.bias, a.seq_start, (const T*)a.state_init, a.S, a.rows,
-                       a.D, run, (T*)a.y, a.y_stride, (T*)a.state_final);
+    // long runs share the fewest rows, short ones fill the chip sooner
+    const long long work = (long long)conv_blocks(a.D) * ((a.rows + 63) / 64);
+    if (work >= 1024) fwd_run<T, W, ACT, 8>(a);
+    else fwd_run<T, W, ACT, 4>(a);
     return hipGetLastError();
 }
 
@@ -269,17 +365,20 @@ hipError_t step_t(const ConvArgs& a) {
     return hipGetLastError();
 }
 
+Pieces bwd_pieces(const int* seq_start, int B, int S, int rows) {
+    return make_pieces(seq_start, B, S, rows, BWD_RUN * BWD_RUNS);
+}
+
 template <typename T, int W, bool ACT>
 hipError_t bwd_t(const ConvArgs& a) {
-    const int run = conv_run(a.B, a.S, a.D, CONV_BWD_RUN);
-    hipLaunchKernelGGL((conv_bwd_kernel<T, W, ACT>), conv_grid(a.B, a.S, a.D, run), dim3(CONV_THREADS), 0, a.stream,
-                       (const T*)a.x, a.x_stride, a.weight, a.bias, a.seq_start, (const T*)a.state_init,
-                       (const T*)a.dy, a.dy_stride, (const T*)a.dstate_final, a.S, a.rows, a.D, run,
+    const Pieces pieces = bwd_pieces(a.seq_start, a.B, a.S, a.rows);
+    hipLaunchKernelGGL((conv_bwd_kernel<T, W, ACT>), dim3((unsigned)((a.D + 255) / 256) * pieces.count()),
+                       dim3(CONV_THREADS), 0, a.stream, (const T*)a.x, a.x_stride, a.weight, a.bias,
+                       (const T*)a.state_init, (const T*)a.dy, a.dy_stride, (const T*)a.dstate_final, pieces, a.D,
                        (T*)a.grad_x, a.grad_x_stride, (T*)a.grad_state, a.ws);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const long long parts = (long long)a.B * ((a.S + run - 1) / run);
-    hipLaunchKernelGGL(conv_sum_kernel<W>, dim3((a.D + 63) / 64, W + 1), dim3(1024), 0, a.stream, a.ws, parts, a.D,
+    hipLaunchKernelGGL(conv_sum_kernel<W>, dim3((a.D + 63) / 64, W + 1), dim3(1024), 0, a.stream, a.ws, pieces.count(), a.D,
                        a.grad_weight, a.grad_bias);
     return hipGetLastError();
 }
@@ -301,9 +400,9 @@ hipError_t launch_conv_fwd(const ConvArgs& a) { CONV_DISPATCH(fwd_t, a) }
 hipError_t launch_conv_step(const ConvArgs& a) { CONV_DISPATCH(step_t, a) }
 hipError_t launch_conv_bwd(const ConvArgs& a) { CONV_DISPATCH(bwd_t, a) }
 
-size_t conv_bwd_workspace_bytes(int B, int S, int D, int width) {
-    const int run = conv_run(B, S, D, CONV_BWD_RUN);
-    return (size_t)B * ((S + run - 1) / run) * (width + 1) * D * sizeof(float);
+size_t conv_bwd_workspace_bytes(int B, int rows, int D, int width) {
+    // as many pieces as packed sequences may need: the size does not depend on seq_start
+    return ((size_t)rows / (BWD_RUN * BWD_RUNS) + B) * (width + 1) * D * sizeof(float);
 }
 
 }  // namespace mlstm

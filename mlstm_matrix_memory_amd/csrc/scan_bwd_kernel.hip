@@ -74,7 +74,7 @@ struct Work {
     };
 
     const BwdParams& p;
-    int b, c, number, tile, tid, lane, wave, d, n0, t_begin, t_end, r0, c4, slot;
+    int b, c, number, tile, tid, lane, wave, d, n0, t_begin, t_end, r0, c4, nc, slot;
     RowRange sq;
     ScanTile ch;
     bool own, live, last;
@@ -108,6 +108,7 @@ struct Work {
         slot = first_slot(sq, b);
         r0 = tid >> 4;
         c4 = (tid & 15) * 4;
+        nc = min(ch.count - c4, 4);
         const long long lo = sq.lo;
         xp = (const T*)p.x + lo * p.x_stride + ch.d0 + c4;
         dtp = (const T*)p.dt + lo * p.dt_stride + ch.d0 + c4;
@@ -285,7 +286,13 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && NL == 4 ? 2 : 1) void scan_bwd_
     __shared__ __align__(16) float part[4][BWD_ROWS][SCAN_TILE];       // o, du, sum_n A w, (unused)
     __shared__ __align__(16) float bcw[NW][BWD_ROWS][2 * NP];          // dB and dC of the wave's channels
     W w(p);
-    if (!w.live) return;
+    float* so = p.sums + (size_t)w.number * (NP + 2) * p.D;    // the piece's sums
+    if (!w.live) {
+        // a number without a piece: its sums are zero
+        if (w.own)
+            for (int k = w.wave; k < NP + 2; k += NW) so[(size_t)k * p.D + w.d] = 0.0f;
+        return;
+    }
     const int lane = w.lane, ng = lane % LPC;
     const int chn = w.wave * (64 / LPC) + lane / LPC;  // the lane's channel in the tile
     const int d = w.ch.d0 + chn, n0 = 4 * ng;          // states n0 + 4 LPC k + j
@@ -418,7 +425,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && NL == 4 ? 2 : 1) void scan_bwd_
 #pragma unroll
         for (int i = 0; i < PASS; ++i) {
             const int r = w.r0 + (NT / 16) * i, t = t0 + r;
-            const int n = t < w.t_end ? w.ch.count - w.c4 : 0;
+            const int n = t < w.t_end ? w.nc : 0;
             f32x4 sum[3];                              // o, du, sum_n A w
 #pragma unroll
             for (int q = 0; q < 3; ++q)
@@ -466,7 +473,6 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && NL == 4 ? 2 : 1) void scan_bwd_
     }
 
     // the piece's sums; those of dskip and dbias lie with the NT / 16 threads of a channel group
-    float* so = p.sums + (size_t)w.number * (NP + 2) * p.D;
     if (own) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
@@ -500,11 +506,9 @@ __global__ __launch_bounds__(1024) void scan_bwd_sums_kernel(const BwdParams p, 
     const int d = blockIdx.x * SCAN_TILE + lane, j = blockIdx.y < p.N ? blockIdx.y : NP + blockIdx.y - p.N;
     float s = 0.0f;
     const int count = p.pieces.count();
-    for (int i = wave; i < count; i += 16) {
-        const Pieces::At at = p.pieces.at(i);
-        const bool there = at.c == 0 || (long long)at.c * p.pieces.length < p.pieces.sequence(at.b).n;
-        if (there && d < p.D) s += p.sums[((size_t)i * (NP + 2) + j) * p.D + d];
-    }
+    if (d < p.D)
+#pragma unroll 8
+        for (int i = wave; i < count; i += 16) s += p.sums[((size_t)i * (NP + 2) + j) * p.D + d];
     sm[wave][lane] = s;
     __syncthreads();
     if (wave != 0 || d >= p.D) return;

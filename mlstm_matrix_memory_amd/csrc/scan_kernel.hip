@@ -21,6 +21,16 @@
 namespace mlstm {
 namespace {
 
+// The channel of a tile at a place of its rows in LDS.  Threads stage four at a time; where the
+// tile's count is no multiple of four the last four places hold its last four channels, some
+// a second time, which are computed and stored twice with the same values.  (Guarding
+// single channels instead made the waves run two paths: packed fp32 rows of 501 channels per
+// group took 53 us against 48 us.)
+__device__ __forceinline__ int scan_channel(int place, int count) {
+    const int shared = count >= 4 && place >= count / 4 * 4 ? (4 - count % 4) % 4 : 0;
+    return place - shared;
+}
+
 struct FwdParams {
     const void* x; const void* dt; const void* Bm; const void* Cm; const void* z;
     long long x_stride, dt_stride, B_stride, C_stride, z_stride, y_stride;
@@ -65,25 +75,27 @@ __global__ __launch_bounds__(128 * NW) void scan_fwd_kernel(const FwdParams p)
         // helper: rows r0 + (NT / 16) i of a tile, channels c4 .. c4 + 3
         if (turns == 0) return;
         const int tid = threadIdx.x - NT, r0 = tid >> 4, c4 = (tid & 15) * 4;
+        const int g4 = ch.count >= 4 ? min(c4, ch.count - 4) : c4;     // the first channel of LDS places c4 ..
         const int bt = tid / NP, bnn = tid % NP;
-        const T* xp = (const T*)p.x + (long long)sq.lo * p.x_stride + ch.d0 + c4;
-        const T* dtp = (const T*)p.dt + (long long)sq.lo * p.dt_stride + ch.d0 + c4;
-        const T* zp = GATE ? (const T*)p.z + (long long)sq.lo * p.z_stride + ch.d0 + c4 : nullptr;
-        T* yp = (T*)p.y + (long long)sq.lo * p.y_stride + ch.d0 + c4;
+        const T* xp = (const T*)p.x + (long long)sq.lo * p.x_stride + ch.d0 + g4;
+        const T* dtp = (const T*)p.dt + (long long)sq.lo * p.dt_stride + ch.d0 + g4;
+        const T* zp = GATE ? (const T*)p.z + (long long)sq.lo * p.z_stride + ch.d0 + g4 : nullptr;
+        T* yp = (T*)p.y + (long long)sq.lo * p.y_stride + ch.d0 + g4;
         const T* bp = (const T*)p.Bm + (long long)sq.lo * p.B_stride + ch.group * p.N + min(bnn, p.N - 1);
         const T* cp = (const T*)p.Cm + (long long)sq.lo * p.C_stride + ch.group * p.N + min(bnn, p.N - 1);
         float bias[4], skip[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            bias[e] = p.dt_bias && c4 + e < ch.count ? p.dt_bias[ch.d0 + c4 + e] : 0.0f;
-            skip[e] = !STATE && p.Dskip && c4 + e < ch.count ? p.Dskip[ch.d0 + c4 + e] : 0.0f;
+            bias[e] = p.dt_bias && g4 + e < ch.count ? p.dt_bias[ch.d0 + g4 + e] : 0.0f;
+            skip[e] = !STATE && p.Dskip && g4 + e < ch.count ? p.Dskip[ch.d0 + g4 + e] : 0.0f;
         }
         // Loads run two tiles ahead.  To know how many accesses lie between a load and its
         // use, and so wait for no later ones, the compiler needs every turn to issue the
         // same: rows past the end are read from the last row and masked when staged.
         auto work = [&](auto full_tag) {
-            constexpr bool FULL = full_tag;            // the tile holds all of its 64 channels
-            const int nc = FULL ? 4 : ch.count - c4;
+            constexpr int FILL = full_tag;             // 2: 64 channels; 1: four to every thread; 0: fewer
+            constexpr bool FULL = FILL > 0;
+            const int nc = ch.count - c4;
             Raw4<T> xn[2][PASS], zn[2][PASS], dtn[2][PASS];
             T bn[2][BCN], cn[2][BCN];
             // x and z of the staged tile and the two before it
@@ -164,7 +176,7 @@ __global__ __launch_bounds__(128 * NW) void scan_fwd_kernel(const FwdParams p)
                         }
                         o.set(e, y[e]);
                     }
-                    if (t < t_end) {
+                    if (t < t_end && (FILL == 2 || c4 < ch.count)) {
                         if (FULL) o.store(yp + t * p.y_stride);
                         else store_row4(yp + t * p.y_stride, o, nc);
                     }
@@ -194,14 +206,15 @@ __global__ __launch_bounds__(128 * NW) void scan_fwd_kernel(const FwdParams p)
             }
             if (!STATE) finish(turns - 1, x0, z0);
         };
-        if (ch.count == SCAN_TILE) work(std::true_type());
-        else work(std::false_type());
+        if (ch.count == SCAN_TILE) work(std::integral_constant<int, 2>());
+        else if (ch.count >= 4) work(std::integral_constant<int, 1>());
+        else work(std::integral_constant<int, 0>());
         return;
     }
 
     // scanner: channel d, states n0 .. n0 + NL - 1
-    const int d = ch.d0 + lane, n0 = wave * NL;
-    const bool own = lane < ch.count;
+    const int d = ch.d0 + scan_channel(lane, ch.count), n0 = wave * NL;
+    const bool own = lane < (ch.count + 3) / 4 * 4 && d < ch.d0 + ch.count;
     float a2[NL], h[NL];
 #pragma unroll
     for (int j = 0; j < NL; ++j) {

@@ -140,10 +140,10 @@ def test_conv_bwd_refusals(lib, kw, words):
 
 
 def test_conv_bwd_workspace(lib):
-    need = b.ssm_conv_bwd_workspace_bytes(2, 8, 64, 4)
+    need = b.ssm_conv_bwd_workspace_bytes(2, 16, 64, 4)
     assert need >= 5 * 64 * 4
     refused(_conv_bwd(lib, n=need - 1), "needed", b.MLSTM_ERR_WORKSPACE)
-    assert b.ssm_conv_bwd_workspace_bytes(2, 0, 64, 4) == 0 and b.ssm_conv_bwd_workspace_bytes(2, 8, 64, 9) == 0
+    assert b.ssm_conv_bwd_workspace_bytes(2, 0, 64, 4) == 0 and b.ssm_conv_bwd_workspace_bytes(2, 16, 64, 9) == 0
 
 
 SCAN = dict(x=P[0], xs=64, dtp=P[1], dts=64, A=P[2], Bm=P[3], bs=16, Cm=P[4], cs=16, skip=P[5], bias=P[6], z=P[7],
