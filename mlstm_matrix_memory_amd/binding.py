@@ -597,18 +597,17 @@ def mlstm_step(q, k, v, i_pre, f_pre, o_pre, C, n, m, h_out=None, stream=None):
 def _row_stride(t, name, trailing: int = 1) -> int:
     """Distance in elements between consecutive rows of t; its last `trailing`
     dimensions make a row, which must be contiguous."""
-    width = 1
-    if t.is_contiguous():
-        for k in t.shape[t.dim() - trailing:]:
-            width *= k
-        return width
     shape, stride = t.shape, t.stride()
-    for k in range(t.dim() - 1, t.dim() - trailing - 1, -1):
+    dims = len(shape)
+    if dims == 2 and trailing == 1 and stride[1] == 1 and shape[0] > 1:
+        return stride[0]
+    width = 1
+    for k in range(dims - 1, dims - trailing - 1, -1):
         if shape[k] != 1 and stride[k] != width:
             raise ValueError(f"the rows of {name} must be contiguous")
         width *= shape[k]
-    step = None
-    for k in range(t.dim() - trailing - 1, -1, -1):
+    step = expect = None
+    for k in range(dims - trailing - 1, -1, -1):
         if shape[k] == 1:
             continue
         if step is None:
@@ -621,12 +620,18 @@ def _row_stride(t, name, trailing: int = 1) -> int:
 
 
 def _check_rows(t, name, shape, dtype, device):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _raw_stream(stream, device):
+    """hipStream_t of the given stream, or of the device's current one, as an integer."""
+    import torch
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _gpu(t, name):
@@ -678,6 +683,12 @@ def _output(t, name, shape, dtype, dev, owned):
     return t
 
 
+def _dense(t, name, shape, dtype, dev):
+    """_check for the operators below: the common case in one comparison."""
+    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        _check(t, name, shape, dtype, dev)
+
+
 def mlstm_rms_norm_bwd_workspace_bytes(rows: int, d: int) -> int:
     return int(load_library().mlstm_rms_norm_bwd_workspace_bytes(rows, d))
 
@@ -686,7 +697,7 @@ def _norm_inputs(x, weight, residual, residual_out, owned):
     import torch
     dev, d = _gpu(x, "x"), x.shape[-1]
     _dtype_code(x)
-    _check(weight, "weight", (d,), torch.float32, dev)
+    _dense(weight, "weight", (d,), torch.float32, dev)
     res_dtype = x.dtype
     if residual is not None:
         _dtype_code(residual)
@@ -698,7 +709,7 @@ def _norm_inputs(x, weight, residual, residual_out, owned):
     elif residual_out is not None:
         res_dtype = residual_out.dtype
     if residual_out is not None:
-        _check(residual_out, "residual_out", x.shape, res_dtype, dev)
+        _dense(residual_out, "residual_out", x.shape, res_dtype, dev)
         _dtype_code(residual_out)
     code = MLSTM_F32 if res_dtype == torch.float32 else MLSTM_BF16
     rows = x.numel() // d if d else 0
@@ -719,10 +730,11 @@ def mlstm_rms_norm_fwd(x, weight, residual=None, eps: float = 1e-5, residual_out
     if y_out is None:
         y_out = torch.empty(x.shape, dtype=x.dtype, device=dev)
         owned.append(y_out)
-    _check(y_out, "y_out", x.shape, x.dtype, dev)
+    else:
+        _dense(y_out, "y_out", x.shape, x.dtype, dev)
     _keep_for_stream(stream, dev, owned)
     _launch("mlstm_rms_norm_fwd", dev, *head, float(eps), _dtype_code(x), res_code, _ptr(residual_out),
-            y_out.data_ptr(), _stream_handle(stream, dev))
+            y_out.data_ptr(), _raw_stream(stream, dev))
     return y_out, x if residual_out is None else residual_out
 
 
@@ -744,11 +756,11 @@ def mlstm_rms_norm_quant(x, weight, residual=None, eps: float = 1e-5, group: int
     if scale_out is None:
         scale_out = torch.empty((*x.shape[:-1], per_row), dtype=torch.float32, device=dev)
         owned.append(scale_out)
-    _check(q_out, "q_out", x.shape, torch.float8_e4m3fn, dev)
-    _check(scale_out, "scale_out", (*x.shape[:-1], per_row), torch.float32, dev)
+    _dense(q_out, "q_out", x.shape, torch.float8_e4m3fn, dev)
+    _dense(scale_out, "scale_out", (*x.shape[:-1], per_row), torch.float32, dev)
     _keep_for_stream(stream, dev, owned)
     _launch("mlstm_rms_norm_quant", dev, *head, float(eps), _dtype_code(x), res_code, group, _ptr(residual_out),
-            q_out.data_ptr(), scale_out.data_ptr(), _stream_handle(stream, dev))
+            q_out.data_ptr(), scale_out.data_ptr(), _raw_stream(stream, dev))
     return q_out, scale_out, x if residual_out is None else residual_out
 
 
@@ -763,10 +775,10 @@ def mlstm_rms_norm_bwd(r, weight, dy, dres=None, eps: float = 1e-5, grad_x=None,
     import torch
     dev, d = _gpu(r, "r"), r.shape[-1]
     res_code, code = _dtype_code(r), _dtype_code(dy)
-    _check(weight, "weight", (d,), torch.float32, dev)
+    _dense(weight, "weight", (d,), torch.float32, dev)
     _check_rows(dy, "dy", r.shape, dy.dtype, dev)
     if dres is not None:
-        _check(dres, "dres", r.shape, r.dtype, dev)
+        _dense(dres, "dres", r.shape, r.dtype, dev)
     owned = []
     if grad_x is None:
         grad_x = torch.empty(r.shape, dtype=dy.dtype, device=dev)
@@ -777,16 +789,16 @@ def mlstm_rms_norm_bwd(r, weight, dy, dres=None, eps: float = 1e-5, grad_x=None,
     if grad_weight is None:
         grad_weight = torch.empty((d,), dtype=torch.float32, device=dev)
         owned.append(grad_weight)
-    _check(grad_x, "grad_x", r.shape, dy.dtype, dev)
+    _dense(grad_x, "grad_x", r.shape, dy.dtype, dev)
     if grad_residual is not None:
-        _check(grad_residual, "grad_residual", r.shape, r.dtype, dev)
-    _check(grad_weight, "grad_weight", (d,), torch.float32, dev)
+        _dense(grad_residual, "grad_residual", r.shape, r.dtype, dev)
+    _dense(grad_weight, "grad_weight", (d,), torch.float32, dev)
     rows = r.numel() // d if d else 0
     ws, ws_bytes = _workspace(workspace, mlstm_rms_norm_bwd_workspace_bytes(rows, d), dev, owned)
     _keep_for_stream(stream, dev, owned)
     _launch("mlstm_rms_norm_bwd", dev, r.data_ptr(), _row_stride(r, "r"), weight.data_ptr(), dy.data_ptr(),
             _row_stride(dy, "dy"), _ptr(dres), rows, d, float(eps), code, res_code, grad_x.data_ptr(),
-            _ptr(grad_residual), grad_weight.data_ptr(), ws, ws_bytes, _stream_handle(stream, dev))
+            _ptr(grad_residual), grad_weight.data_ptr(), ws, ws_bytes, _raw_stream(stream, dev))
     return grad_x, grad_x if grad_residual is None else grad_residual, grad_weight
 
 
@@ -805,7 +817,7 @@ def _batch(x, seq_start, max_len, dev):
         raise ValueError("x must be 2-D [rows, D] with seq_start")
     if seq_start.dim() != 1 or seq_start.numel() < 2:
         raise ValueError("seq_start must be 1-D with a start per sequence and the last one's end")
-    _check(seq_start, "seq_start", (seq_start.numel(),), torch.int32, dev)
+    _dense(seq_start, "seq_start", (seq_start.numel(),), torch.int32, dev)
     if max_len is None:
         raise ValueError("seq_start needs max_len, the length of the longest sequence")
     return seq_start.numel() - 1, int(max_len), x.shape[0]
@@ -823,19 +835,19 @@ def ssm_conv_fwd(x, weight, bias=None, act: int = SSM_ACT_SWISH, state_init=None
     dev, dt = _gpu(x, "x"), _dtype_code(x)
     B, S, rows = _batch(x, seq_start, max_len, dev)
     D, W = x.shape[-1], weight.shape[-1]
-    _check(weight, "weight", (D, W), torch.float32, dev)
+    _dense(weight, "weight", (D, W), torch.float32, dev)
     if bias is not None:
-        _check(bias, "bias", (D,), torch.float32, dev)
+        _dense(bias, "bias", (D,), torch.float32, dev)
     if state_init is not None:
-        _check(state_init, "state_init", (B, W - 1, D), x.dtype, dev)
+        _dense(state_init, "state_init", (B, W - 1, D), x.dtype, dev)
     owned = []
     y_out = _output(y_out, "y_out", x.shape, x.dtype, dev, owned)
     state_final = _output(state_final, "state_final", (B, max(W - 1, 0), D), x.dtype, dev, owned)
-    _check(state_final, "state_final", (B, max(W - 1, 0), D), x.dtype, dev)
+    _dense(state_final, "state_final", (B, max(W - 1, 0), D), x.dtype, dev)
     _keep_for_stream(stream, dev, owned)
     _launch("ssm_conv_fwd", dev, x.data_ptr(), _row_stride(x, "x"), weight.data_ptr(), _ptr(bias), _ptr(seq_start),
             _ptr(state_init), B, S, rows, D, W, int(act), dt, y_out.data_ptr(), _row_stride(y_out, "y_out"),
-            state_final.data_ptr(), _stream_handle(stream, dev))
+            state_final.data_ptr(), _raw_stream(stream, dev))
     return y_out, state_final
 
 
@@ -847,15 +859,15 @@ def ssm_conv_step(x, weight, state, bias=None, act: int = SSM_ACT_SWISH, y_out=N
     if x.dim() != 2:
         raise ValueError("x must be 2-D [B, D]")
     (B, D), W = x.shape, weight.shape[-1]
-    _check(weight, "weight", (D, W), torch.float32, dev)
+    _dense(weight, "weight", (D, W), torch.float32, dev)
     if bias is not None:
-        _check(bias, "bias", (D,), torch.float32, dev)
-    _check(state, "state", (B, W - 1, D), x.dtype, dev)
+        _dense(bias, "bias", (D,), torch.float32, dev)
+    _dense(state, "state", (B, W - 1, D), x.dtype, dev)
     owned = []
     y_out = _output(y_out, "y_out", x.shape, x.dtype, dev, owned)
     _keep_for_stream(stream, dev, owned)
     _launch("ssm_conv_step", dev, x.data_ptr(), _row_stride(x, "x"), weight.data_ptr(), _ptr(bias), B, D, W, int(act),
-            dt, state.data_ptr(), y_out.data_ptr(), _row_stride(y_out, "y_out"), _stream_handle(stream, dev))
+            dt, state.data_ptr(), y_out.data_ptr(), _row_stride(y_out, "y_out"), _raw_stream(stream, dev))
     return y_out
 
 
@@ -875,12 +887,12 @@ def ssm_conv_bwd(x, weight, dy, bias=None, act: int = SSM_ACT_SWISH, state_init=
     dev, dt = _gpu(x, "x"), _dtype_code(x)
     B, S, rows = _batch(x, seq_start, max_len, dev)
     D, W = x.shape[-1], weight.shape[-1]
-    _check(weight, "weight", (D, W), torch.float32, dev)
+    _dense(weight, "weight", (D, W), torch.float32, dev)
     if bias is not None:
-        _check(bias, "bias", (D,), torch.float32, dev)
+        _dense(bias, "bias", (D,), torch.float32, dev)
     for t, name in ((state_init, "state_init"), (dstate_final, "dstate_final")):
         if t is not None:
-            _check(t, name, (B, W - 1, D), x.dtype, dev)
+            _dense(t, name, (B, W - 1, D), x.dtype, dev)
     _check_rows(dy, "dy", x.shape, x.dtype, dev)
     owned = []
     grad_x = _output(grad_x, "grad_x", x.shape, x.dtype, dev, owned)
@@ -893,7 +905,7 @@ def ssm_conv_bwd(x, weight, dy, bias=None, act: int = SSM_ACT_SWISH, state_init=
     _launch("ssm_conv_bwd", dev, x.data_ptr(), _row_stride(x, "x"), weight.data_ptr(), _ptr(bias), _ptr(seq_start),
             _ptr(state_init), dy.data_ptr(), _row_stride(dy, "dy"), _ptr(dstate_final), B, S, rows, D, W, int(act), dt,
             grad_x.data_ptr(), _row_stride(grad_x, "grad_x"), grad_weight.data_ptr(), _ptr(grad_bias),
-            _ptr(grad_state), ws, ws_bytes, _stream_handle(stream, dev))
+            _ptr(grad_state), ws, ws_bytes, _raw_stream(stream, dev))
     return grad_x, grad_weight, grad_bias, grad_state
 
 
@@ -906,12 +918,12 @@ def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, batch, dev):
     lead, G = tuple(x.shape[:-1]), B.shape[-2]
     _check_rows(x, "x", (*lead, width), x.dtype, dev)
     _check_rows(dt, "dt", (*lead, width), x.dtype, dev)
-    _check(A, "A", (width, N), torch.float32, dev)
+    _dense(A, "A", (width, N), torch.float32, dev)
     for t, name in ((B, "B"), (C, "C")):
         _check_rows(t, name, (*lead, G, N), x.dtype, dev)
     for t, name in ((D, "D"), (dt_bias, "dt_bias")):
         if t is not None:
-            _check(t, name, (width,), torch.float32, dev)
+            _dense(t, name, (width,), torch.float32, dev)
     if z is not None:
         _check_rows(z, "z", (*lead, width), x.dtype, dev)
     args = [x.data_ptr(), _row_stride(x, "x"), dt.data_ptr(), _row_stride(dt, "dt"), A.data_ptr(),
@@ -937,16 +949,16 @@ def ssm_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = 
     batch, S, rows = _batch(x, seq_start, max_len, dev)
     args, width, G, N = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, batch, dev)
     if h_init is not None:
-        _check(h_init, "h_init", (batch, width, N), torch.float32, dev)
+        _dense(h_init, "h_init", (batch, width, N), torch.float32, dev)
     owned = []
     y_out = _output(y_out, "y_out", x.shape, x.dtype, dev, owned)
     h_final = _output(h_final, "h_final", (batch, width, N), torch.float32, dev, owned)
-    _check(h_final, "h_final", (batch, width, N), torch.float32, dev)
+    _dense(h_final, "h_final", (batch, width, N), torch.float32, dev)
     ws, ws_bytes = _workspace(workspace, ssm_scan_fwd_workspace_bytes(batch, S, rows, width, G, N), dev, owned)
     _keep_for_stream(stream, dev, owned)
     _launch("ssm_scan_fwd", dev, *args, _ptr(seq_start), _ptr(h_init), batch, S, rows, width, G, N, int(softplus), code,
             y_out.data_ptr(), _row_stride(y_out, "y_out"), h_final.data_ptr(), ws, ws_bytes,
-            _stream_handle(stream, dev))
+            _raw_stream(stream, dev))
     return y_out, h_final
 
 
@@ -959,12 +971,12 @@ def ssm_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None, softplus: bool = T
         raise ValueError("x must be 2-D [batch, D]")
     batch = x.shape[0]
     args, width, G, N = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, batch, dev)
-    _check(h, "h", (batch, width, N), torch.float32, dev)
+    _dense(h, "h", (batch, width, N), torch.float32, dev)
     owned = []
     y_out = _output(y_out, "y_out", x.shape, x.dtype, dev, owned)
     _keep_for_stream(stream, dev, owned)
     _launch("ssm_step", dev, *args, batch, width, G, N, int(softplus), code, h.data_ptr(), y_out.data_ptr(),
-            _row_stride(y_out, "y_out"), _stream_handle(stream, dev))
+            _row_stride(y_out, "y_out"), _raw_stream(stream, dev))
     return y_out
 
 
@@ -988,7 +1000,7 @@ def ssm_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, softplus: boo
     _check_rows(dy, "dy", x.shape, x.dtype, dev)
     for t, name in ((h_init, "h_init"), (dh_final, "dh_final")):
         if t is not None:
-            _check(t, name, (batch, width, N), torch.float32, dev)
+            _dense(t, name, (batch, width, N), torch.float32, dev)
     owned = []
     grad_x = _output(grad_x, "grad_x", x.shape, x.dtype, dev, owned)
     grad_dt = _output(grad_dt, "grad_dt", x.shape, x.dtype, dev, owned)
@@ -1010,5 +1022,5 @@ def ssm_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, softplus: boo
             grad_x.data_ptr(), _row_stride(grad_x, "grad_x"), grad_dt.data_ptr(), _row_stride(grad_dt, "grad_dt"),
             _ptr(grad_z), 0 if grad_z is None else _row_stride(grad_z, "grad_z"),
             grad_B.data_ptr(), _row_stride(grad_B, "grad_B", 2), grad_C.data_ptr(), _row_stride(grad_C, "grad_C", 2),
-            grad_A.data_ptr(), _ptr(grad_D), _ptr(grad_bias), _ptr(grad_h), ws, ws_bytes, _stream_handle(stream, dev))
+            grad_A.data_ptr(), _ptr(grad_D), _ptr(grad_bias), _ptr(grad_h), ws, ws_bytes, _raw_stream(stream, dev))
     return grad_x, grad_dt, grad_A, grad_B, grad_C, grad_D, grad_z, grad_bias, grad_h

@@ -146,8 +146,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(
     }
 }
 
-// The workgroup's rows are blockIdx.x * RPW + (its row group), in steps of the grid;
-// each row group sums dweight over its rows in registers and writes one part.
+// The workgroup's rows are blockIdx.x * RPW + (its row group), in steps of the grid; each
+// row group sums dweight over its rows in registers, and the workgroup writes one part.
 template <typename T, typename RT, int TPR, int CPT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(
     const RT* __restrict__ r, long long r_stride, const float* __restrict__ weight,
@@ -157,8 +157,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(
     constexpr int THREADS = TPR < 256 ? 256 : TPR;
     constexpr int RPW = THREADS / TPR;
     __shared__ float red[2][THREADS / 64];
+    __shared__ __align__(16) float wsum[RPW > 1 ? RPW : 1][RPW > 1 ? TPR * CPT * 8 : 8];
     const int tl = threadIdx.x % TPR;
-    const int part = blockIdx.x * RPW + threadIdx.x / TPR;
     float dw[CPT][8];
 #pragma unroll
     for (int c = 0; c < CPT; ++c)
@@ -168,21 +168,26 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(
     for (long long base = (long long)blockIdx.x * RPW; base < rows; base += (long long)gridDim.x * RPW) {
         const long long row = base + threadIdx.x / TPR;
         const bool live = row < rows;
-        float rv[CPT][8], gv[CPT][8];
-        float ss = 0.0f, sv = 0.0f;
+        // all of the row's loads first: grad_residual may be dres
+        Raw8<RT> a[CPT], add[CPT];
+        Raw8<T> g[CPT];
 #pragma unroll
         for (int c = 0; c < CPT; ++c) {
             const int col = 8 * (tl + TPR * c);
             const int n = live ? d - col : 0;
-            const Raw8<RT> a = load_row8(r + (live ? row * r_stride : 0) + col, n);
-            const Raw8<T> g = load_row8(dy + (live ? row * dy_stride : 0) + col, n);
-            const Raw8<float> w = load_row8(weight + col, d - col);
+            a[c] = load_row8(r + (live ? row * r_stride : 0) + col, n);
+            g[c] = load_row8(dy + (live ? row * dy_stride : 0) + col, n);
+            add[c].zero();
+            if (dres) add[c] = load_row8(dres + (live ? row * d : 0) + col, n);
+        }
+        float ss = 0.0f, sv = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) {
+            const Raw8<float> w = load_row8(weight + 8 * (tl + TPR * c), d - 8 * (tl + TPR * c));
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                rv[c][e] = a.get(e);
-                gv[c][e] = g.get(e);
-                ss += rv[c][e] * rv[c][e];
-                sv += rv[c][e] * gv[c][e] * w.get(e);
+                ss += a[c].get(e) * a[c].get(e);
+                sv += a[c].get(e) * g[c].get(e) * w.get(e);
             }
         }
         ss = row_reduce<TPR, false>(ss, red[0]);
@@ -194,29 +199,42 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(
             const int col = 8 * (tl + TPR * c);
             const int n = live ? d - col : 0;
             const Raw8<float> w = load_row8(weight + col, d - col);
-            Raw8<RT> add;
-            add.zero();
-            if (dres) add = load_row8(dres + (live ? row * d : 0) + col, n);
             Raw8<T> gx;
             Raw8<RT> gr;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float g = k * (gv[c][e] * w.get(e) - rv[c][e] * t) + add.get(e);
-                gx.set(e, g);
-                gr.set(e, g);
-                if (live) dw[c][e] += gv[c][e] * rv[c][e] * k;
+                const float v = k * (g[c].get(e) * w.get(e) - a[c].get(e) * t) + add[c].get(e);
+                gx.set(e, v);
+                gr.set(e, v);
+                if (live) dw[c][e] += g[c].get(e) * a[c].get(e) * k;
             }
             if (grad_x) store_row8(grad_x + (live ? row * d : 0) + col, gx, n);
             if (grad_residual) store_row8(grad_residual + (live ? row * d : 0) + col, gr, n);
         }
     }
+    if (RPW > 1) {
 #pragma unroll
-    for (int c = 0; c < CPT; ++c) {
-        const int col = 8 * (tl + TPR * c);
-        Raw8<float> o;
+        for (int c = 0; c < CPT; ++c)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o.set(e, dw[c][e]);
-        store_row8(parts + (size_t)part * d + col, o, d - col);
+            for (int e = 0; e < 8; e += 4)
+                *reinterpret_cast<f32x4*>(&wsum[threadIdx.x / TPR][8 * (tl + TPR * c) + e]) =
+                    f32x4{dw[c][e], dw[c][e + 1], dw[c][e + 2], dw[c][e + 3]};
+        __syncthreads();
+        for (int col = threadIdx.x; col < d; col += THREADS) {
+            float v = wsum[0][col];
+#pragma unroll
+            for (int k = 1; k < RPW; ++k) v += wsum[k][col];
+            parts[(size_t)blockIdx.x * d + col] = v;
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) {
+            const int col = 8 * (tl + TPR * c);
+            Raw8<float> o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o.set(e, dw[c][e]);
+            store_row8(parts + (size_t)blockIdx.x * d + col, o, d - col);
+        }
     }
 }
 
@@ -249,12 +267,14 @@ int norm_variant(int d) {
     return d <= 512 ? 0 : d <= 1024 ? 1 : d <= 2048 ? 2 : d <= 4096 ? 3 : d <= 8192 ? 4 : 5;
 }
 
-// workgroups of the backward: enough to fill the chip, few enough that the parts of
-// dweight stay small beside the rows
+// Workgroups of the backward: two to a compute unit.  bf16 rows with an fp32 sum, 512, 1024 and
+// 2048 workgroups: (rows, d) = (16384, 768) 47.5, 55.6 and 53.4 us, (8192, 2048) 55.4, 58.6 and
+// 64.4 us; all bf16 (8192, 4096) 64.1, 72.2 and 70.3 us.
+constexpr int NORM_BWD_GRID = 512;
 int norm_bwd_grid(int rows, int d) {
     const int rpw = norm_variant_rows(norm_variant(d));
     const long long wanted = (rows + rpw - 1) / rpw;
-    return (int)(wanted < 512 ? wanted : 512);
+    return (int)(wanted < NORM_BWD_GRID ? wanted : NORM_BWD_GRID);
 }
 
 #define NORM_DISPATCH(v, CALL)          \
@@ -294,7 +314,7 @@ hipError_t launch_bwd_t(const NormArgs& a) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(sum_parts_kernel, dim3((a.d + 63) / 64), dim3(1024), 0, a.stream, a.ws,
-                       (int)grid.x * norm_variant_rows(v), a.d, a.grad_weight);
+                       (int)grid.x, a.d, a.grad_weight);
     return hipGetLastError();
 }
 
@@ -311,7 +331,7 @@ hipError_t launch_norm_fwd(const NormArgs& a) {
 }
 
 size_t norm_bwd_workspace_bytes(int rows, int d) {
-    return (size_t)norm_bwd_grid(rows, d) * norm_variant_rows(norm_variant(d)) * d * sizeof(float);
+    return (size_t)norm_bwd_grid(rows, d) * d * sizeof(float);
 }
 
 hipError_t launch_norm_bwd(const NormArgs& a) {

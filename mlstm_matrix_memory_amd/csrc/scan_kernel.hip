@@ -285,8 +285,9 @@ __global__ __launch_bounds__(128 * NW) void scan_fwd_kernel(const FwdParams p)
 }
 
 // One row per sequence: a lane holds 4 states of a channel (one 16-byte access), LPC
-// lanes a channel.  Bound by the state's HBM traffic, 8 bytes per state.
-template <typename T, int LPC>
+// lanes a channel, of SEQS sequences.  Bound by the state's HBM traffic, 8 bytes per state:
+// several sequences to a thread keep as many loads in flight, and read A once for them.
+template <typename T, int LPC, int SEQS>
 __global__ __launch_bounds__(256) void ssm_step_kernel(
     const T* __restrict__ x, long long x_stride, const T* __restrict__ dt, long long dt_stride,
     const float* __restrict__ A, const T* __restrict__ Bm, long long B_stride, const T* __restrict__ Cm,
@@ -295,50 +296,71 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(
     T* __restrict__ y, long long y_stride)
 {
     const int q = threadIdx.x % LPC, n = 4 * q;
-    const long long ch = (long long)blockIdx.x * (256 / LPC) + threadIdx.x / LPC;
-    const bool live = ch < (long long)B * D;           // a channel's lanes are live or not together
-    const long long b = live ? ch / D : 0;
-    const int d = live ? (int)(ch % D) : 0, g = d / (D / G);
-    const int cnt = live ? min(max(N - n, 0), 4) : 0;
-    const float v = to_f32(dt[b * dt_stride + d]) + (dt_bias ? dt_bias[d] : 0.0f);
-    const float s = softplus ? softplus_hw(v) : v;
-    const float xv = to_f32(x[b * x_stride + d]), u = s * xv;
-    float* hp = h + ((size_t)b * D + d) * N + n;
-    const float* ap = A + (size_t)d * N + n;
-    const T* bp = Bm + b * B_stride + g * N + n;
-    const T* cp = Cm + b * C_stride + g * N + n;
-    f32x4 hv = {0, 0, 0, 0}, av = hv;
-    if (cnt == 4) {
-        hv = *reinterpret_cast<const f32x4_u*>(hp);
-        av = *reinterpret_cast<const f32x4_u*>(ap);
-    } else {
+    const int sets = (B + SEQS - 1) / SEQS;            // this thread's sequences: set, set + sets, ...
+    const long long id = (long long)blockIdx.x * (256 / LPC) + threadIdx.x / LPC;
+    const bool in = id < (long long)sets * D;          // a channel's lanes are in or not together
+    const int set = in ? (int)(id / D) : 0, d = in ? (int)(id % D) : 0, g = d / (D / G);
+    const int cnt = min(max(N - n, 0), 4);
+    f32x4 hv[SEQS], av = {0, 0, 0, 0};
+    Raw4<T> bv[SEQS], cv[SEQS];
+    T xv[SEQS], dtv[SEQS], zv[SEQS];
+    bool live[SEQS];
 #pragma unroll
-        for (int j = 0; j < 3; ++j)
-            if (j < cnt) { hv[j] = hp[j]; av[j] = ap[j]; }
-    }
-    float o = 0.0f;
+    for (int k = 0; k < SEQS; ++k) {
+        const long long b = set + (long long)k * sets;
+        live[k] = in && b < B;
+        const long long r = live[k] ? b : 0;
+        const float* hp = h + ((size_t)r * D + d) * N + n;
+        if (cnt == 4) {
+            hv[k] = *reinterpret_cast<const f32x4_u*>(hp);
+        } else {
+            hv[k] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float bv = j < cnt ? to_f32(bp[j]) : 0.0f, cv = j < cnt ? to_f32(cp[j]) : 0.0f;
-        hv[j] = fmaf(__builtin_amdgcn_exp2f(s * (av[j] * LOG2E)), hv[j], u * bv);
-        o = fmaf(cv, hv[j], o);
-    }
-    if (cnt == 4) {
-        *reinterpret_cast<f32x4_u*>(hp) = hv;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 3; ++j)
-            if (j < cnt) hp[j] = hv[j];
-    }
-#pragma unroll
-    for (int off = LPC / 2; off > 0; off >>= 1) o += __shfl_xor(o, off, 64);
-    if (live && q == 0) {
-        if (Dskip) o = fmaf(Dskip[d], xv, o);
-        if (z) {
-            const float zv = to_f32(z[b * z_stride + d]);
-            o *= zv * sigmoid_hw(zv);
+            for (int j = 0; j < 3; ++j)
+                if (j < cnt) hv[k][j] = hp[j];
         }
-        y[b * y_stride + d] = from_f32<T>(o);
+        bv[k] = load_row4(Bm + r * B_stride + g * N + n, cnt);
+        cv[k] = load_row4(Cm + r * C_stride + g * N + n, cnt);
+        xv[k] = x[r * x_stride + d];
+        dtv[k] = dt[r * dt_stride + d];
+        if (z) zv[k] = z[r * z_stride + d];
+    }
+    {
+        const Raw4<float> a = load_row4(A + (size_t)d * N + n, cnt);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) av[j] = a.get(j) * LOG2E;
+    }
+    const float bias = dt_bias ? dt_bias[d] : 0.0f, skip = Dskip ? Dskip[d] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < SEQS; ++k) {
+        const long long b = set + (long long)k * sets;
+        const float v = to_f32(dtv[k]) + bias, xf = to_f32(xv[k]);
+        const float s = softplus ? softplus_hw(v) : v, u = s * xf;
+        float o = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            hv[k][j] = fmaf(__builtin_amdgcn_exp2f(s * av[j]), hv[k][j], u * bv[k].get(j));
+            o = fmaf(cv[k].get(j), hv[k][j], o);
+        }
+#pragma unroll
+        for (int off = LPC / 2; off > 0; off >>= 1) o += __shfl_xor(o, off, 64);
+        if (!live[k]) continue;
+        float* hp = h + ((size_t)b * D + d) * N + n;
+        if (cnt == 4) {
+            *reinterpret_cast<f32x4_u*>(hp) = hv[k];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (j < cnt) hp[j] = hv[k][j];
+        }
+        if (q == 0) {
+            o = fmaf(skip, xf, o);
+            if (z) {
+                const float zf = to_f32(zv[k]);
+                o *= zf * sigmoid_hw(zf);
+            }
+            y[b * y_stride + d] = from_f32<T>(o);
+        }
     }
 }
 
@@ -407,14 +429,15 @@ hipError_t fwd_t(const ScanArgs& a) {
     return hipGetLastError();
 }
 
-template <typename T>
-hipError_t step_t(const ScanArgs& a) {
-    const long long ch = (long long)a.B * a.D;
-#define STEP_CALL(LPC)                                                                                                \
-    hipLaunchKernelGGL((ssm_step_kernel<T, LPC>), dim3((unsigned)((ch * LPC + 255) / 256)), dim3(256), 0, a.stream,   \
-                       (const T*)a.x, a.x_stride, (const T*)a.dt, a.dt_stride, a.A, (const T*)a.Bm, a.B_stride,       \
-                       (const T*)a.Cm, a.C_stride, a.Dskip, a.dt_bias, (const T*)a.z, a.z_stride, a.B, a.D, a.G, a.N, \
-                       a.softplus, a.h_final, (T*)a.y, a.y_stride)
+constexpr long long STEP_SEQS_FROM = 1LL << 21;
+template <typename T, int SEQS>
+void step_launch(const ScanArgs& a) {
+    const long long ch = (long long)((a.B + SEQS - 1) / SEQS) * a.D;
+#define STEP_CALL(LPC)                                                                                                 \
+    hipLaunchKernelGGL((ssm_step_kernel<T, LPC, SEQS>), dim3((unsigned)((ch * LPC + 255) / 256)), dim3(256), 0,        \
+                       a.stream, (const T*)a.x, a.x_stride, (const T*)a.dt, a.dt_stride, a.A, (const T*)a.Bm,          \
+                       a.B_stride, (const T*)a.Cm, a.C_stride, a.Dskip, a.dt_bias, (const T*)a.z, a.z_stride, a.B,     \
+                       a.D, a.G, a.N, a.softplus, a.h_final, (T*)a.y, a.y_stride)
     switch (scan_padded_states(a.N)) {
         case 4: STEP_CALL(1); break;
         case 8: STEP_CALL(2); break;
@@ -423,6 +446,14 @@ hipError_t step_t(const ScanArgs& a) {
         default: STEP_CALL(16); break;
     }
 #undef STEP_CALL
+}
+
+template <typename T>
+hipError_t step_t(const ScanArgs& a) {
+    // (sequences, channels) at N = 16, bf16, one and two sequences to a thread: (256, 2048) 15.9 and 15.4 us,
+    // (64, 2048) 5.9 and 5.5, (32, 2048) 4.3 and 4.3, (16, 2048) 3.5 and 3.8 (four: 15.5, 6.1, 5.1, 4.9)
+    if ((long long)a.B * a.D * scan_padded_states(a.N) >= STEP_SEQS_FROM) step_launch<T, 2>(a);
+    else step_launch<T, 1>(a);
     return hipGetLastError();
 }
 

@@ -225,3 +225,27 @@ def test_block_operators_exported(lib):
                  "ssm_conv_bwd_workspace_bytes", "ssm_scan_fwd", "ssm_step", "ssm_scan_fwd_workspace_bytes",
                  "ssm_scan_bwd", "ssm_scan_bwd_workspace_bytes"):
         assert name in b.header_symbols() and hasattr(lib, name) and callable(getattr(pkg, name))
+
+
+def test_binding_refuses_before_any_call():
+    """Shapes, dtypes and layouts are checked on any device; these calls reach no library function."""
+    import torch
+    import mlstm_matrix_memory_amd as pkg
+    x, w = torch.zeros(2, 8, 64), torch.zeros(64, 4)
+    with pytest.raises(ValueError, match="GPU"):
+        pkg.ssm_conv_fwd(x, w)
+    with pytest.raises(ValueError, match="GPU"):
+        pkg.mlstm_rms_norm_fwd(x, torch.ones(64))
+    assert b._row_stride(torch.zeros(5, 7), "t") == 7 and b._row_stride(torch.zeros(5, 14)[:, :7], "t") == 14
+    assert b._row_stride(torch.zeros(1, 14)[:, :7], "t") == 7
+    assert b._row_stride(torch.zeros(2, 3, 2, 8), "t", 2) == 16
+    assert b._row_stride(torch.zeros(2, 3, 40)[..., 8:24].view(2, 3, 2, 8), "t", 2) == 40
+    assert b._row_stride(torch.zeros(3, 1, 9), "t") == 9 and b._row_stride(torch.zeros(3, 2, 9)[:, :1], "t") == 18
+    for bad in (torch.zeros(7, 5).t(), torch.zeros(2, 8, 64)[:, :, ::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            b._row_stride(bad, "t")
+    with pytest.raises(ValueError, match="uniform"):
+        b._row_stride(torch.zeros(2, 8, 64)[:, :4], "t")
+    with pytest.raises(ValueError, match="contiguous"):
+        b._row_stride(torch.zeros(4, 1).expand(4, 6), "t")       # a broadcast row
+    assert b._row_stride(torch.zeros(1, 6).expand(4, 6), "t") == 0     # a broadcast batch: refused by the library (stride)

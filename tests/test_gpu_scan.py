@@ -119,3 +119,26 @@ def test_extreme_step_sizes_and_gates():
     torch.cuda.synchronize()
     assert np.all(np.isfinite(to_np(y))) and np.all(np.isfinite(to_np(final)))
     check(c, y, final)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_short_and_one_long_sequence(dtype):
+    import torch
+    # piece numbers of packed sequences: empty ones first, last and in a row, single rows, one long
+    lengths = [0, 0, 1, 900, 0, 17, 64, 63, 65, 1, 1, 128, 0]
+    starts = list(np.cumsum([0] + lengths))
+    announce(f"scan fwd packed {lengths} {dtype}")
+    c = make(37, 8, dtype, 15, packed=starts)
+    y, final = forward(c)
+    torch.cuda.synchronize()
+    check(c, y, final, joins=True)
+
+
+def test_repeated_calls_give_the_same_bits():
+    import torch
+    announce("scan fwd three times, B=1 S=900 D=200 N=16")
+    c = make(200, 16, "bf16", 13, B=1, S=900)
+    first = [t.clone() for t in forward(c)]
+    for _ in range(2):
+        for p, q in zip(first, forward(c)):
+            assert torch.equal(p, q)

@@ -85,6 +85,32 @@ def test_long_sequences_cut_into_pieces(dtype):
         check(c, got, joins=True)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_short_and_one_long_sequence(dtype):
+    import torch
+    lengths = [0, 0, 1, 900, 0, 17, 64, 63, 65, 1, 1, 128, 0]
+    starts = list(np.cumsum([0] + lengths))
+    announce(f"scan bwd packed {lengths} {dtype}")
+    c = make(37, 8, dtype, 15, packed=starts)
+    got = backward(c)
+    torch.cuda.synchronize()
+    check(c, got, joins=True)
+
+
+def test_starts_outside_the_tensor_are_clamped():
+    import torch
+    from mlstm_matrix_memory_amd import ssm_scan_bwd
+    announce("scan bwd with seq_start entries below 0, above rows and a length above max_len")
+    c = make(20, 16, "f32", 5, packed=[0, 4, 30])
+    start = torch.tensor([-5, 4, 1000], dtype=torch.int32, device="cuda")
+    left = {f"grad_{k}": torch.full(c[k].shape, 7.0, device="cuda") for k in ("x", "dt", "z", "B", "C")}
+    got = ssm_scan_bwd(*(dev(c, k) for k in ("x", "dt", "A", "B", "C", "dy", "D", "z", "dt_bias")), h_init=dev(c, "h"),
+                       dh_final=dev(c, "dh"), seq_start=start, max_len=20, **left)
+    torch.cuda.synchronize()
+    c["spans"] = [(0, 4), (4, 24)]
+    assert all(np.all(r == 7) for r in check(c, got))
+
+
 def test_repeated_calls_give_the_same_bits():
     import torch
     announce("scan bwd three times, B=2 S=300 D=200 N=16")
