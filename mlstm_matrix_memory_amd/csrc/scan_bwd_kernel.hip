@@ -540,23 +540,28 @@ __global__ __launch_bounds__(256) void scan_bwd_bc_kernel(const BwdParams p, int
 }
 
 // Rows per piece.  Cutting costs the R and the sums of the first kernel (about a tenth of the
-// whole), and pays where whole sequences would leave the 512 places (two workgroups to a
-// compute unit) unfilled: (sequences, rows, channels) = (16, 1024, 2048), 512 workgroups, took
+// whole), and pays where whole sequences would leave places unfilled, at N = 16 512 (two workgroups
+// to a compute unit): (sequences, rows, channels) = (16, 1024, 2048), 512 workgroups, took
 // 646 us whole and 719 us in four pieces; (4, 2048, 4096), 256 workgroups, 941 us whole, 775, 743
 // and 732 us in 2, 4 and 8; (8, 2048, 1536) 917 us whole, 748, 594, 629 and 555 us in 2, 4, 6 and
 // 8.  The 6 lose because their workgroups fill the places 2.25 times: so the number is taken that
 // makes rounds * rows the least, with 24 rows for a piece's start, and among numbers within a
 // twentieth of that the largest.
-constexpr int PLACES = 512, WHOLE_FROM = 448, MOST_WORKGROUPS = 2048, SHORTEST_PIECE = 64, START_ROWS = 24;
-int piece_rows(int S, int rows, int D, int G) {
+// The places by N: up to 8 states workgroups of one or two waves fit four times to a compute unit
+// ((1, 2048, 1536) at N = 4 took 111 us for 512 places and 76 us for 1024), above 16 their
+// registers leave room for one ((8, 1024, 2048) at N = 32 took 910 us in four pieces and
+// 784 us whole).
+constexpr int SHORTEST_PIECE = 48, START_ROWS = 24;
+int piece_rows(int S, int rows, int D, int G, int N) {
+    const int places = N <= 8 ? 1024 : N <= 16 ? 512 : 256;
     // packed sequences count by the rows that there are
-    const long long groups = (long long)scan_tiles(D, G) * ((rows + S - 1) / S);
+    const long long groups = ((long long)scan_tiles(D, G) * rows + S / 2) / S;
     const int whole = (S + BWD_ROWS - 1) / BWD_ROWS * BWD_ROWS;
-    if (groups >= WHOLE_FROM || whole <= SHORTEST_PIECE) return whole;
+    if (groups >= places - places / 8 || whole <= SHORTEST_PIECE) return whole;
     auto length = [&](int n) { return (int)(((S + n - 1) / n + BWD_ROWS - 1) / BWD_ROWS * BWD_ROWS); };
-    auto cost = [&](int n) { return (groups * n + PLACES - 1) / PLACES * (length(n) + START_ROWS); };
+    auto cost = [&](int n) { return (groups * n + places - 1) / places * (length(n) + START_ROWS); };
     long long least = cost(1);
-    const int most = (int)(MOST_WORKGROUPS / groups);
+    const int most = (int)(4 * places / groups);
     for (int n = 2; n <= most && length(n) >= SHORTEST_PIECE; ++n)
         if (cost(n) < least) least = cost(n);
     int best = 1;
@@ -573,7 +578,7 @@ struct BwdPlan {
 BwdPlan plan(const int* seq_start, int B, int S, int rows, int D, int G, int N) {
     const size_t NP = scan_padded_states(N);
     BwdPlan f = {};
-    f.pieces = make_pieces(seq_start, B, S, rows, piece_rows(S, rows, D, G));
+    f.pieces = make_pieces(seq_start, B, S, rows, piece_rows(S, rows, D, G, N));
     f.cut = f.pieces.length < S;
     size_t at = 0;
     auto take = [&](size_t n) { const size_t o = at; at += (n + 63) / 64 * 64; return o; };

@@ -371,13 +371,15 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(
 // workgroups: on one MI355X (2, 1024, 4096) (sequences, rows, channels; 128 workgroups) took
 // 76 us uncut and 67 us in six pieces, (8, 2048, 1536) (192 workgroups) 148 us uncut and 173 us
 // in eight; (1, 32768, 2048) 2512 us uncut, 646, 501, 483 and 499 us in 8, 16, 32 and 64 pieces.
-constexpr int CUT_BELOW = 144, CUT_TO = 1024, SHORTEST_PIECE = 64;
-int piece_rows(int S, int rows, int D, int G) {
+// Up to 4 states, where a workgroup is two waves, cutting pays longer: (8, 1024, 2048), 256
+// workgroups, took 117 us uncut and 69 us in four pieces at N = 4, 69 and 92 us at N = 8.
+constexpr int CUT_BELOW = 144, CUT_BELOW_4 = 320, CUT_TO = 1024, SHORTEST_PIECE = 64;
+int piece_rows(int S, int rows, int D, int G, int N) {
     // packed sequences count by the rows that there are
-    const long long groups = (long long)scan_tiles(D, G) * ((rows + S - 1) / S);
+    const long long groups = ((long long)scan_tiles(D, G) * rows + S / 2) / S;
     const int whole = (S + 31) / 32 * 32;
-    if (groups > CUT_BELOW) return whole;
-    const long long n = (CUT_TO + groups - 1) / groups;
+    if (groups > (N <= 4 ? CUT_BELOW_4 : CUT_BELOW)) return whole;
+    const long long n = groups > 0 ? (CUT_TO + groups - 1) / groups : CUT_TO;
     const int length = (int)(((S + n - 1) / n + 15) / 16 * 16);
     return length < SHORTEST_PIECE ? (SHORTEST_PIECE < whole ? SHORTEST_PIECE : whole) : length;
 }
@@ -389,7 +391,7 @@ struct FwdPlan {
 };
 FwdPlan plan(const int* seq_start, int B, int S, int rows, int D, int G, int N) {
     FwdPlan f = {};
-    f.pieces = make_pieces(seq_start, B, S, rows, piece_rows(S, rows, D, G));
+    f.pieces = make_pieces(seq_start, B, S, rows, piece_rows(S, rows, D, G, N));
     if (f.pieces.length < S) {
         // as many as packed sequences may need, so that a workspace's size does not depend on seq_start
         const size_t count = (size_t)rows / f.pieces.length + B;
