@@ -29,14 +29,17 @@ struct Region {
     size_t align;              // of its elements
     bool out;                  // written by the call
     bool optional;
+    long long given;           // the stride as given, in elements
 };
 
 inline Region dense(const void* p, size_t elems, size_t el, const char* name, bool out = false, bool optional = false) {
-    return Region{p, 1, elems * el, elems * el, name, el, out, optional};
+    return Region{p, 1, elems * el, elems * el, name, el, out, optional, (long long)elems};
 }
 inline Region strided(const void* p, size_t rows, size_t width, long long stride, size_t el, const char* name,
                       bool out = false, bool optional = false) {
-    return Region{p, rows, width * el, (size_t)stride * el, name, el, out, optional};
+    // a stride whose bytes could pass 64 bits counts as 0, which no row has
+    const size_t bytes = stride < 0 || stride > (1LL << 50) ? 0 : (size_t)stride * el;
+    return Region{p, rows, width * el, bytes, name, el, out, optional, stride};
 }
 
 // null pointers, element alignment, row strides
@@ -48,9 +51,9 @@ inline mlstm_status regions(const Region* r, int n) {
         }
         if (reinterpret_cast<uintptr_t>(r[i].p) % r[i].align)
             return fail(MLSTM_ERR_INVALID_ARG, "%s is not %zu-byte aligned", r[i].name, r[i].align);
-        if (r[i].stride < r[i].width || r[i].stride > ((size_t)1 << 40))
+        if (r[i].stride < r[i].width || r[i].stride > ((size_t)1 << 50) / (r[i].rows ? r[i].rows : 1))
             return fail(MLSTM_ERR_INVALID_ARG, "%s_stride=%lld is out of range for rows of %zu elements", r[i].name,
-                        (long long)(r[i].stride / r[i].align), r[i].width / r[i].align);
+                        r[i].given, r[i].width / r[i].align);
     }
     return MLSTM_OK;
 }
@@ -95,7 +98,8 @@ inline mlstm_status workspace(const void* ws, size_t given, size_t need, size_t 
 }
 
 // sizes of a batch of sequences over rows of D channels
-constexpr int MAX_SEQUENCES = 65535, MAX_ROWS = 1 << 30;
+constexpr int MAX_SEQUENCES = 65535, MAX_ROWS = 1 << 30, MAX_CHANNELS = 1 << 24;
+constexpr long long MAX_GRID = 0x7fffffffLL;
 inline mlstm_status batch(int B, int S, int rows, int D, const int* seq_start) {
     if (B < 1 || S < 1 || rows < 1 || D < 1)
         return fail(MLSTM_ERR_INVALID_ARG, "B=%d, S=%d, rows=%d, D=%d must all be >= 1", B, S, rows, D);
@@ -103,8 +107,11 @@ inline mlstm_status batch(int B, int S, int rows, int D, const int* seq_start) {
     if (!seq_start && (long long)B * S != rows)
         return fail(MLSTM_ERR_INVALID_ARG, "rows=%d is not B*S=%lld", rows, (long long)B * S);
     if (S > rows) return fail(MLSTM_ERR_INVALID_ARG, "S=%d exceeds rows=%d", S, rows);
-    // row indexes, also rounded up to tiles of rows, are 32-bit in the kernels
-    if (rows > MAX_ROWS || (long long)rows * D > (1LL << 40)) return fail(MLSTM_ERR_UNSUPPORTED, "tensor too large");
+    // row and channel indexes, also rounded up to tiles, are 32-bit in the kernels, and so is the
+    // number of workgroups: at most one per 64 channels and 16 rows (or sequence)
+    if (rows > MAX_ROWS || D > MAX_CHANNELS || (long long)rows * D > (1LL << 40) ||
+        (long long)((D + 63) / 64) * (rows / 16 + B) > MAX_GRID)
+        return fail(MLSTM_ERR_UNSUPPORTED, "tensor too large");
     if (reinterpret_cast<uintptr_t>(seq_start) % 4)
         return fail(MLSTM_ERR_INVALID_ARG, "seq_start is not 4-byte aligned");
     return MLSTM_OK;

@@ -163,6 +163,18 @@ struct Pieces {
         return At{b, number - (min(max(seq_start[b], 0), rows) / length + b)};
     }
     __device__ __forceinline__ RowRange sequence(int b) const { return sequence_rows(seq_start, b, S, rows); }
+    // whether a sequence has the row
+    __device__ __forceinline__ bool has(int row) const {
+        if (!seq_start) return true;
+        int b = 0, end = B;              // the last sequence that starts at the row or before it
+        while (end - b > 1) {
+            const int mid = (b + end) >> 1;
+            if (seq_start[mid] <= row) b = mid;
+            else end = mid;
+        }
+        const RowRange sq = sequence(b);
+        return row >= sq.lo && row < sq.lo + sq.n;
+    }
 };
 inline Pieces make_pieces(const int* seq_start, int B, int S, int rows, int length) {
     return Pieces{seq_start, B, S, rows, length, (S + length - 1) / length};

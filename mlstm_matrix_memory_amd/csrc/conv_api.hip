@@ -71,7 +71,7 @@ mlstm_status ssm_conv_step(const void* x, long long x_stride, const float* weigh
 }
 
 size_t ssm_conv_bwd_workspace_bytes(int B, int rows, int D, int width) {
-    if (B < 1 || rows < 1 || D < 1 || B > MAX_SEQUENCES || rows > MAX_ROWS) return 0;
+    if (B < 1 || rows < 1 || D < 1 || B > MAX_SEQUENCES || rows > MAX_ROWS || D > MAX_CHANNELS) return 0;
     if (check_conv(width, SSM_ACT_NONE, MLSTM_F32) != MLSTM_OK) return 0;
     return mlstm::conv_bwd_workspace_bytes(B, rows, D, width);
 }

@@ -11,9 +11,12 @@ mlstm_status check_scan(int B, int rows, int D, int G, int N) {
     if (G < 1 || D % G) return fail(MLSTM_ERR_INVALID_ARG, "D=%d is not a multiple of G=%d", D, G);
     if (N < 1 || N > mlstm::SCAN_MAX_N)
         return fail(MLSTM_ERR_INVALID_ARG, "N=%d must lie in [1, %d]", N, mlstm::SCAN_MAX_N);
-    // workgroups: tiles of 64 channels times pieces, of which there are at most rows / 16 + B
-    const long long tiles = (long long)G * ((D / G + 63) / 64);
-    if (tiles * (rows / 16 + B) > 0x7fffffffLL) return fail(MLSTM_ERR_UNSUPPORTED, "batch too large");
+    // workgroups: tiles of 64 channels times pieces, of which there are at most rows / 16 + B; 256
+    // states each in the step; 256 elements of B and C each in the backward's sums
+    const long long tiles = (long long)G * ((D / G + 63) / 64), bc = (long long)G * N;
+    if (tiles * (rows / 16 + B) > MAX_GRID || bc > MAX_CHANNELS || rows * bc / 128 >= MAX_GRID ||
+        (long long)B * D / 64 >= MAX_GRID)
+        return fail(MLSTM_ERR_UNSUPPORTED, "batch too large");
     return MLSTM_OK;
 }
 
@@ -62,6 +65,7 @@ mlstm::ScanArgs make(const Inputs& i) {
 
 bool sizes_ok(int B, int S, int rows, int D, int G, int N) {
     return B >= 1 && S >= 1 && D >= 1 && B <= MAX_SEQUENCES && rows >= 1 && rows <= MAX_ROWS && S <= rows &&
+           D <= MAX_CHANNELS &&
            check_scan(B, rows, D, G, N) == MLSTM_OK;
 }
 

@@ -523,14 +523,10 @@ __global__ __launch_bounds__(1024) void scan_bwd_sums_kernel(const BwdParams p, 
 template <typename T>
 __global__ __launch_bounds__(256) void scan_bwd_bc_kernel(const BwdParams p, int NP)
 {
-    const int b = blockIdx.y;
-    const RowRange sq = p.pieces.sequence(b);
     const int width = 2 * p.G * p.N;
-    const long long at = (long long)blockIdx.x * 256 + threadIdx.x;
-    const long long t = at / width;
-    if (t >= sq.n) return;
+    const long long at = (long long)blockIdx.x * 256 + threadIdx.x, row = at / width;
+    if (row >= p.pieces.rows || !p.pieces.has((int)row)) return;
     const int e = (int)(at % width), k = e / (p.G * p.N), g = e / p.N % p.G, n = e % p.N;
-    const long long row = sq.lo + t;
     const int per = scan_tiles(p.D, p.G) / p.G;
     const float* src = p.bc + ((size_t)g * per * p.pieces.rows + row) * (2 * NP) + k * NP + n;
     float s = 0.0f;
@@ -628,8 +624,8 @@ hipError_t bwd_t(const ScanArgs& a) {
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(scan_bwd_sums_kernel, dim3((a.D + 63) / 64, a.N + 2), dim3(1024), 0, a.stream, p, NP);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    const long long elems = (long long)a.S * 2 * a.G * a.N;
-    hipLaunchKernelGGL(scan_bwd_bc_kernel<T>, dim3((unsigned)((elems + 255) / 256), a.B), dim3(256), 0, a.stream, p, NP);
+    const long long elems = (long long)a.rows * 2 * a.G * a.N;
+    hipLaunchKernelGGL(scan_bwd_bc_kernel<T>, dim3((unsigned)((elems + 255) / 256)), dim3(256), 0, a.stream, p, NP);
     return hipGetLastError();
 }
 

@@ -106,6 +106,19 @@ def test_too_many_sequences(lib):
     refused(_conv(lib, B=65536, S=1, rows=65536), "65536", b.MLSTM_ERR_UNSUPPORTED)
 
 
+def test_sizes_past_the_kernels_indexes(lib):
+    unsupported = b.MLSTM_ERR_UNSUPPORTED
+    refused(_conv(lib, D=(1 << 24) + 1, xs=1 << 25, ys=1 << 25), "too large", unsupported)
+    refused(_conv(lib, B=1, S=(1 << 30) + 1, rows=(1 << 30) + 1), "too large", unsupported)
+    refused(_conv(lib, xs=1 << 58), "x_stride")
+    refused(_conv(lib, xs=(1 << 62) + 64), "x_stride=46116860184273879")      # its bytes wrap to a small number
+    refused(_conv(lib, xs=-64), "x_stride=-64")
+    refused(_scan(lib, B=65535, S=1, rows=65535, D=1 << 24, xs=1 << 24, dts=1 << 24, zs=1 << 24, ys=1 << 24), "too large",
+            unsupported)
+    assert b.ssm_conv_bwd_workspace_bytes(2, 16, (1 << 24) + 1, 4) == 0
+    assert b.ssm_scan_bwd_workspace_bytes(1, 1 << 30, 1 << 30, 1 << 24, 1, 16) == 0
+
+
 def test_column_ranges_of_one_buffer_are_apart(lib):
     # y behind x in rows of one width: accepted so far as to reach the next check
     refused(_conv(lib, xs=128, y=P[0] + 2 * 64, ys=128, final=P[3]), "state_final overlaps state_init")

@@ -142,3 +142,35 @@ def test_repeated_calls_give_the_same_bits():
     for _ in range(2):
         for p, q in zip(first, forward(c)):
             assert torch.equal(p, q)
+
+
+def test_rows_far_apart():
+    """Rows 8.4 million elements apart: offsets past 32 bits in every tensor give the bits of dense rows."""
+    import torch
+    from mlstm_matrix_memory_amd import ssm_conv_bwd, ssm_conv_fwd, ssm_scan_bwd, ssm_scan_fwd
+    announce("scan and convolution, forward and backward, over rows 8.4 million elements apart (300 rows)")
+    c = make(64, 16, "bf16", 16, B=1, S=300, state=False)
+    t = {k: dev(c, k) for k in ("x", "dt", "A", "B", "C", "D", "z", "dt_bias", "dy")}
+    apart = 8_400_000
+    wide = torch.zeros(1, 300, apart, dtype=torch.bfloat16, device="cuda")
+
+    def far(place, like):
+        v = wide[:, :, place * 64:place * 64 + like[0, 0].numel()].view(like.shape)
+        v.copy_(like)
+        return v
+
+    f = {k: far(i, t[k]) for i, k in enumerate(("x", "dt", "z", "dy", "B", "C"))}
+    out = [far(6 + i, torch.zeros_like(t["x"])) for i in range(6)]
+    outB, outC = far(12, torch.zeros_like(t["B"])), far(13, torch.zeros_like(t["C"]))
+    par = dict(D=t["D"], dt_bias=t["dt_bias"])
+    w = torch.randn(64, 4, device="cuda")
+    a = [ssm_scan_fwd(t["x"], t["dt"], t["A"], t["B"], t["C"], z=t["z"], **par)[0],
+         ssm_conv_fwd(t["x"], w)[0], ssm_conv_bwd(t["x"], w, t["dy"])[0],
+         *ssm_scan_bwd(t["x"], t["dt"], t["A"], t["B"], t["C"], t["dy"], z=t["z"], **par)[:8]]
+    g = ssm_scan_bwd(f["x"], f["dt"], t["A"], f["B"], f["C"], f["dy"], z=f["z"], grad_x=out[3], grad_dt=out[4],
+                     grad_z=out[5], grad_B=outB, grad_C=outC, **par)
+    b = [ssm_scan_fwd(f["x"], f["dt"], t["A"], f["B"], f["C"], z=f["z"], y_out=out[0], **par)[0],
+         ssm_conv_fwd(f["x"], w, y_out=out[1])[0], ssm_conv_bwd(f["x"], w, f["dy"], grad_x=out[2])[0], *g[:8]]
+    torch.cuda.synchronize()
+    for i, (u, v) in enumerate(zip(a, b)):
+        assert torch.equal(u, v), i
