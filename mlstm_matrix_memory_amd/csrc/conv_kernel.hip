@@ -165,9 +165,14 @@ __global__ __launch_bounds__(64) void conv_step_kernel(
 // the rows before it (its initial state).  A thread owns 4 channels here: taps, sums and
 // windows of 8 took 396 registers, one wave to a SIMD.  The workgroup, 64 threads of channels
 // by 4 runs, adds its runs' dw and dbias in LDS and writes one part of them.
-constexpr int BWD_RUN = 29;                            // with W = 4, 8 blocks of 4 rows
+// Rows of a run: with W = 4 29 make 8 blocks of 4.  13, 29 and 45 rows: (8, 2048, 1536) 50.4, 43.6
+// and 46.7 us, packed rows of 1537 channels (6583 rows) 32.1, 28.3 and 45.7 us.
+constexpr int BWD_RUN = 29;
 constexpr int BWD_RUNS = CONV_THREADS / 64;
-template <typename T, int W, bool ACT>
+// FINAL: a gradient of the final state comes in.  (A template parameter because a load under a
+// condition makes the compiler wait, where its value is used, for every load in flight: bf16
+// rows of (8, 2048, 1536) took 52.6 us so and 43.6 us without it.)
+template <typename T, int W, bool ACT, bool FINAL>
 __global__ __launch_bounds__(CONV_THREADS) void conv_bwd_kernel(
     const T* __restrict__ x, long long x_stride, const float* __restrict__ weight, const float* __restrict__ bias,
     const T* __restrict__ state_init, const T* __restrict__ dy, long long dy_stride,
@@ -198,7 +203,7 @@ __global__ __launch_bounds__(CONV_THREADS) void conv_bwd_kernel(
         const T* xs = x + sq.lo * x_stride + c;
         const T* gs = dy + sq.lo * dy_stride + c;
         const T* st = state_init ? state_init + (size_t)at.b * (W - 1) * D + c : nullptr;
-        const T* df = dstate_final ? dstate_final + (size_t)at.b * (W - 1) * D + c : nullptr;
+        const T* df = FINAL ? dstate_final + (size_t)at.b * (W - 1) * D + c : nullptr;
         T* dxs = dx + sq.lo * dx_stride + c;
         T* gst = grad_state ? grad_state + (size_t)at.b * (W - 1) * D + c : nullptr;
         float w[W][4], bs[4], past[W - 1][4], dp[W][4];
@@ -256,7 +261,7 @@ __global__ __launch_bounds__(CONV_THREADS) void conv_bwd_kernel(
                     const int held = s - (sq.n - (W - 1));       // its place in the final state, if >= 0
                     Raw4<T> more, o;
                     more.zero();
-                    if (df && held >= 0 && held < W - 1) more = load_row4(df + (size_t)held * D, n);
+                    if (FINAL && held >= 0 && held < W - 1) more = load_row4(df + (size_t)held * D, n);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float v = t < sq.n ? xv[i].get(e) : 0.0f;
@@ -350,7 +355,9 @@ void fwd_run(const ConvArgs& a) {
 
 template <typename T, int W, bool ACT>
 hipError_t fwd_t(const ConvArgs& a) {
-    // long runs share the fewest rows, short ones fill the chip sooner
+    // Long runs share the fewest rows, short ones fill the chip sooner.  bf16, rows of a half, runs of
+    // 4, 8 and 16: (4, 2048, 4096) 30.5, 28.3 and 32.0 us, (8, 2048, 1536) 24.5, 23.3 and 22.1,
+    // (1, 2048, 2048) 7.2, 7.2 and 8.9, (1, 512, 2048) 4.8, 5.8 and 7.6 us.
     const long long work = (long long)conv_blocks(a.D) * ((a.rows + 63) / 64);
     if (work >= 1024) fwd_run<T, W, ACT, 8>(a);
     else fwd_run<T, W, ACT, 4>(a);
@@ -369,10 +376,10 @@ Pieces bwd_pieces(const int* seq_start, int B, int S, int rows) {
     return make_pieces(seq_start, B, S, rows, BWD_RUN * BWD_RUNS);
 }
 
-template <typename T, int W, bool ACT>
-hipError_t bwd_t(const ConvArgs& a) {
+template <typename T, int W, bool ACT, bool FINAL>
+hipError_t bwd_run(const ConvArgs& a) {
     const Pieces pieces = bwd_pieces(a.seq_start, a.B, a.S, a.rows);
-    hipLaunchKernelGGL((conv_bwd_kernel<T, W, ACT>), dim3((unsigned)((a.D + 255) / 256) * pieces.count()),
+    hipLaunchKernelGGL((conv_bwd_kernel<T, W, ACT, FINAL>), dim3((unsigned)((a.D + 255) / 256) * pieces.count()),
                        dim3(CONV_THREADS), 0, a.stream, (const T*)a.x, a.x_stride, a.weight, a.bias,
                        (const T*)a.state_init, (const T*)a.dy, a.dy_stride, (const T*)a.dstate_final, pieces, a.D,
                        (T*)a.grad_x, a.grad_x_stride, (T*)a.grad_state, a.ws);
@@ -381,6 +388,11 @@ hipError_t bwd_t(const ConvArgs& a) {
     hipLaunchKernelGGL(conv_sum_kernel<W>, dim3((a.D + 63) / 64, W + 1), dim3(1024), 0, a.stream, a.ws, pieces.count(), a.D,
                        a.grad_weight, a.grad_bias);
     return hipGetLastError();
+}
+
+template <typename T, int W, bool ACT>
+hipError_t bwd_t(const ConvArgs& a) {
+    return a.dstate_final ? bwd_run<T, W, ACT, true>(a) : bwd_run<T, W, ACT, false>(a);
 }
 
 #define CONV_DISPATCH(F, a)                                                                   \
