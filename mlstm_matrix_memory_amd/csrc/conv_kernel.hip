@@ -166,7 +166,7 @@ __global__ __launch_bounds__(64) void conv_step_kernel(
 // windows of 8 took 396 registers, one wave to a SIMD.  The workgroup, 64 threads of channels
 // by 4 runs, adds its runs' dw and dbias in LDS and writes one part of them.
 // Rows of a run: with W = 4 29 make 8 blocks of 4.  13, 29 and 45 rows: (8, 2048, 1536) 50.4, 43.6
-// and 46.7 us, packed rows of 1537 channels (6583 rows) 32.1, 28.3 and 45.7 us.
+// and 46.7 us, packed rows of 1537 channels (6598 rows) 32.1, 28.3 and 45.7 us.
 constexpr int BWD_RUN = 29;
 constexpr int BWD_RUNS = CONV_THREADS / 64;
 // FINAL: a gradient of the final state comes in.  (A template parameter because a load under a
