@@ -435,6 +435,8 @@ mlstm_status slstm_fwd(const float *x_pre, const void *R, int B, int NH, int S, 
  *   - Outputs may not share bytes with inputs or each other except where said.
  *     Column ranges of one buffer with the same row stride do not count as sharing.
  *   - No atomics: repeated calls on the same inputs give the same bits.
+ *   - At most 2^30 rows, 2^24 channels and 65535 sequences, and 2^32 - 1 threads in a
+ *     launch; larger calls are MLSTM_ERR_UNSUPPORTED before anything is enqueued.
  */
 typedef enum ssm_act {
     SSM_ACT_NONE = 0,

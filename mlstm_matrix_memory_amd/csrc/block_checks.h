@@ -118,6 +118,8 @@ inline mlstm_status batch(int B, int S, int rows, int D, const int* seq_start) {
 }
 
 inline mlstm_status launched(hipError_t e) {
+    if (e == hipErrorInvalidConfiguration)
+        return fail(MLSTM_ERR_UNSUPPORTED, "batch too large: more threads than one launch takes");
     if (e != hipSuccess) return fail(MLSTM_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
     return ok();
 }

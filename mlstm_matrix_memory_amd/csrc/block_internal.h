@@ -181,6 +181,10 @@ inline Pieces make_pieces(const int* seq_start, int B, int S, int rows, int leng
 }
 
 // ---- launchers -------------------------------------------------------------------
+// One launch takes at most 2^32 - 1 threads; the launchers return
+// hipErrorInvalidConfiguration, before any kernel of the call, where it would be more.
+inline bool launchable(long long groups, int threads) { return groups <= 0xffffffffLL / threads; }
+
 struct NormArgs {
     const void* x; long long x_stride;               // rows of the input (backward: r)
     const void* residual; long long residual_stride; // or null

@@ -346,8 +346,7 @@ __global__ __launch_bounds__(1024) void conv_sum_kernel(const float* __restrict_
 int conv_blocks(int D) { return ((D + 7) / 8 + CONV_LANES - 1) / CONV_LANES; }
 
 template <typename T, int W, bool ACT, int RUN>
-void fwd_run(const ConvArgs& a) {
-    const Pieces pieces = make_pieces(a.seq_start, a.B, a.S, a.rows, RUN * CONV_RUNS);
+void fwd_run(const ConvArgs& a, const Pieces& pieces) {
     hipLaunchKernelGGL((conv_fwd_kernel<T, W, ACT, RUN>), dim3((unsigned)conv_blocks(a.D) * pieces.count()),
                        dim3(CONV_THREADS), 0, a.stream, (const T*)a.x, a.x_stride, a.weight, a.bias,
                        (const T*)a.state_init, pieces, a.D, (T*)a.y, a.y_stride, (T*)a.state_final);
@@ -359,14 +358,18 @@ hipError_t fwd_t(const ConvArgs& a) {
     // 4, 8 and 16: (4, 2048, 4096) 30.5, 28.3 and 32.0 us, (8, 2048, 1536) 24.5, 23.3 and 22.1,
     // (1, 2048, 2048) 7.2, 7.2 and 8.9, (1, 512, 2048) 4.8, 5.8 and 7.6 us.
     const long long work = (long long)conv_blocks(a.D) * ((a.rows + 63) / 64);
-    if (work >= 1024) fwd_run<T, W, ACT, 8>(a);
-    else fwd_run<T, W, ACT, 4>(a);
+    const int run = work >= 1024 ? 8 : 4;
+    const Pieces pieces = make_pieces(a.seq_start, a.B, a.S, a.rows, run * CONV_RUNS);
+    if (!launchable((long long)conv_blocks(a.D) * pieces.count(), CONV_THREADS)) return hipErrorInvalidConfiguration;
+    if (run == 8) fwd_run<T, W, ACT, 8>(a, pieces);
+    else fwd_run<T, W, ACT, 4>(a, pieces);
     return hipGetLastError();
 }
 
 template <typename T, int W, bool ACT>
 hipError_t step_t(const ConvArgs& a) {
     const long long threads = (long long)a.B * ((a.D + 7) / 8);
+    if (!launchable((threads + 63) / 64, 64)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((conv_step_kernel<T, W, ACT>), dim3((unsigned)((threads + 63) / 64)), dim3(64), 0, a.stream,
                        (const T*)a.x, a.x_stride, a.weight, a.bias, a.B, a.D, (T*)a.state_final, (T*)a.y, a.y_stride);
     return hipGetLastError();
@@ -379,6 +382,7 @@ Pieces bwd_pieces(const int* seq_start, int B, int S, int rows) {
 template <typename T, int W, bool ACT, bool FINAL>
 hipError_t bwd_run(const ConvArgs& a) {
     const Pieces pieces = bwd_pieces(a.seq_start, a.B, a.S, a.rows);
+    if (!launchable((long long)((a.D + 255) / 256) * pieces.count(), CONV_THREADS)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((conv_bwd_kernel<T, W, ACT, FINAL>), dim3((unsigned)((a.D + 255) / 256) * pieces.count()),
                        dim3(CONV_THREADS), 0, a.stream, (const T*)a.x, a.x_stride, a.weight, a.bias,
                        (const T*)a.state_init, (const T*)a.dy, a.dy_stride, (const T*)a.dstate_final, pieces, a.D,

@@ -8,6 +8,7 @@ using mlstm::fail;
 
 mlstm_status check_norm(int rows, int d, float eps, mlstm_dtype dt, mlstm_dtype res_dt) {
     if (rows < 1) return fail(MLSTM_ERR_INVALID_ARG, "rows=%d must be >= 1", rows);
+    if (rows > MAX_ROWS) return fail(MLSTM_ERR_UNSUPPORTED, "rows=%d exceeds %d", rows, MAX_ROWS);
     if (d < 1 || d > mlstm::NORM_MAX_D)
         return fail(MLSTM_ERR_INVALID_ARG, "d=%d must lie in [1, %d]", d, mlstm::NORM_MAX_D);
     if (!(eps >= 0.0f) || eps > 3.0e38f) return fail(MLSTM_ERR_INVALID_ARG, "eps=%g must be finite and >= 0", eps);

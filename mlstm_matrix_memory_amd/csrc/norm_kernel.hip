@@ -292,6 +292,7 @@ hipError_t launch_fwd_t(const NormArgs& a) {
     const int v = norm_variant(a.d);
     const int rpw = norm_variant_rows(v);
     const dim3 grid((a.rows + rpw - 1) / rpw);
+    if (!launchable(grid.x, v < 5 ? 256 : 1024)) return hipErrorInvalidConfiguration;
 #define NORM_CALL(TPR, CPT)                                                                                     \
     hipLaunchKernelGGL((norm_fwd_kernel<T, RT, TPR, CPT, QUANT>), grid, dim3(TPR < 256 ? 256 : TPR), 0,        \
                        a.stream, (const T*)a.x, a.x_stride, (const RT*)a.residual, a.residual_stride, a.weight, \

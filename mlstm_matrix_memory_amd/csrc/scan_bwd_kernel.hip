@@ -610,11 +610,14 @@ hipError_t bwd_t(const ScanArgs& a) {
     p.dA = a.grad_A; p.dskip = a.grad_Dskip; p.dbias = a.grad_dt_bias; p.dh_init = a.grad_h;
     p.state = a.ws + f.state; p.before = a.ws + f.before; p.bc = a.ws + f.bc; p.sums = a.ws + f.sums;
     p.piece_h = a.ws + f.piece_h; p.piece_g = a.ws + f.piece_g; p.piece_s = a.ws + f.piece_s;
-    const dim3 grid((unsigned)scan_tiles(a.D, a.G) * f.pieces.count());
+    const long long elems = (long long)a.rows * 2 * a.G * a.N, groups = (long long)scan_tiles(a.D, a.G) * f.pieces.count();
+    if (!launchable((elems + 255) / 256, 256)) return hipErrorInvalidConfiguration;
+    const dim3 grid((unsigned)groups);
 #define SCAN_LAUNCH(NW, NL, CUT)                                                                               \
     hipLaunchKernelGGL((scan_bwd_states_kernel<T, NW, NL, CUT>), grid, dim3(64 * NW), 0, a.stream, p);         \
     hipLaunchKernelGGL((scan_bwd_kernel<T, NW, NL, CUT>), grid, dim3(64 * NW), 0, a.stream, p)
 #define SCAN_CALL(NW, NL)                         \
+    if (!launchable(groups, 64 * NW)) return hipErrorInvalidConfiguration; \
     if (f.cut) { SCAN_LAUNCH(NW, NL, true); }     \
     else { SCAN_LAUNCH(NW, NL, false); }
     SCAN_DISPATCH_N(a.N, SCAN_CALL)
@@ -624,7 +627,6 @@ hipError_t bwd_t(const ScanArgs& a) {
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(scan_bwd_sums_kernel, dim3((a.D + 63) / 64, a.N + 2), dim3(1024), 0, a.stream, p, NP);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    const long long elems = (long long)a.rows * 2 * a.G * a.N;
     hipLaunchKernelGGL(scan_bwd_bc_kernel<T>, dim3((unsigned)((elems + 255) / 256)), dim3(256), 0, a.stream, p, NP);
     return hipGetLastError();
 }

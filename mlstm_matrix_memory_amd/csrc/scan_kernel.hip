@@ -412,14 +412,15 @@ hipError_t fwd_t(const ScanArgs& a) {
     p.D = a.D; p.G = a.G; p.N = a.N; p.softplus = a.softplus;
     p.y = a.y; p.h_final = a.h_final;
     p.piece_h = a.ws; p.piece_s = a.ws + f.state;
-    const unsigned grid = (unsigned)scan_tiles(a.D, a.G) * f.pieces.count();
+    const long long grid = (long long)scan_tiles(a.D, a.G) * f.pieces.count();
     // Tiles of 32 rows have half the barriers but take 104 KB of LDS, one workgroup to a compute
     // unit; of 16 rows three fit.  (4, 2048, 4096), 256 workgroups, uncut: 157 us against 177 us;
     // (16, 1024, 2048), 512 workgroups: 165 us against 139 us.
     const bool deep = !f.state && grid <= 256;
 #define SCAN_LAUNCH(NW, NL, ROWS, STATE, GATE) \
-    hipLaunchKernelGGL((scan_fwd_kernel<T, NW, NL, ROWS, STATE, GATE>), dim3(grid), dim3(128 * NW), 0, a.stream, p)
+    hipLaunchKernelGGL((scan_fwd_kernel<T, NW, NL, ROWS, STATE, GATE>), dim3((unsigned)grid), dim3(128 * NW), 0, a.stream, p)
 #define SCAN_CALL(NW, NL)                                    \
+    if (!launchable(grid, 128 * NW)) return hipErrorInvalidConfiguration; \
     if (f.state) SCAN_LAUNCH(NW, NL, 16, true, false);       \
     if (deep && a.z) SCAN_LAUNCH(NW, NL, 32, false, true);   \
     else if (deep) SCAN_LAUNCH(NW, NL, 32, false, false);    \
@@ -433,8 +434,9 @@ hipError_t fwd_t(const ScanArgs& a) {
 
 constexpr long long STEP_SEQS_FROM = 1LL << 21;
 template <typename T, int SEQS>
-void step_launch(const ScanArgs& a) {
+hipError_t step_launch(const ScanArgs& a) {
     const long long ch = (long long)((a.B + SEQS - 1) / SEQS) * a.D;
+    if (!launchable((ch * (scan_padded_states(a.N) / 4) + 255) / 256, 256)) return hipErrorInvalidConfiguration;
 #define STEP_CALL(LPC)                                                                                                 \
     hipLaunchKernelGGL((ssm_step_kernel<T, LPC, SEQS>), dim3((unsigned)((ch * LPC + 255) / 256)), dim3(256), 0,        \
                        a.stream, (const T*)a.x, a.x_stride, (const T*)a.dt, a.dt_stride, a.A, (const T*)a.Bm,          \
@@ -448,15 +450,15 @@ void step_launch(const ScanArgs& a) {
         default: STEP_CALL(16); break;
     }
 #undef STEP_CALL
+    return hipGetLastError();
 }
 
 template <typename T>
 hipError_t step_t(const ScanArgs& a) {
     // (sequences, channels) at N = 16, bf16, one and two sequences to a thread: (256, 2048) 15.9 and 15.4 us,
     // (64, 2048) 5.9 and 5.5, (32, 2048) 4.3 and 4.3, (16, 2048) 3.5 and 3.8 (four: 15.5, 6.1, 5.1, 4.9)
-    if ((long long)a.B * a.D * scan_padded_states(a.N) >= STEP_SEQS_FROM) step_launch<T, 2>(a);
-    else step_launch<T, 1>(a);
-    return hipGetLastError();
+    if ((long long)a.B * a.D * scan_padded_states(a.N) >= STEP_SEQS_FROM) return step_launch<T, 2>(a);
+    return step_launch<T, 1>(a);
 }
 
 }  // namespace

@@ -262,3 +262,32 @@ def test_binding_refuses_before_any_call():
     with pytest.raises(ValueError, match="contiguous"):
         b._row_stride(torch.zeros(4, 1).expand(4, 6), "t")       # a broadcast row
     assert b._row_stride(torch.zeros(1, 6).expand(4, 6), "t") == 0     # a broadcast batch: refused by the library (stride)
+
+
+def _far(a, **kw):
+    """The call's pointers 2^46 bytes apart (never dereferenced), for tensors larger than their usual distance."""
+    a = {k: (v // 0x10000000 << 46) if isinstance(v, int) and v >= 0x10000000 and v % 0x10000000 == 0 else v
+         for k, v in a.items()}
+    return dict(a, **kw)
+
+
+def test_norm_rows_past_32_bit_indexes(lib):
+    rows = (1 << 31) - 1
+    refused(_norm(lib, rows=rows, d=1, xs=1, rs=1), "exceeds", b.MLSTM_ERR_UNSUPPORTED)
+    refused(_norm_bwd(lib, rows=rows, d=1, rs=1, ds=1), "exceeds", b.MLSTM_ERR_UNSUPPORTED)
+    assert b.mlstm_rms_norm_bwd_workspace_bytes(rows, 1) == 0
+
+
+def test_more_threads_than_a_launch_takes(lib):
+    """Refused before any kernel: 2^32 threads or more."""
+    words, code = "more threads than one launch takes", b.MLSTM_ERR_UNSUPPORTED
+    far = _far(dict(x=P[0], res=P[1], w=P[2], rout=P[3], y=P[4], scale=P[5]))
+    for quant in (False, True):                      # a wave to a row: 2^26 rows
+        refused(_norm(lib, quant=quant, rows=1 << 26, d=8, xs=8, rs=8, **far), words, code)
+    # 65535 sequences of one row: a workgroup each for every 64 channels (256 of the convolution)
+    B, D, wide = 65535, 1 << 14, dict(xs=1 << 14, ys=1 << 14)
+    conv = _far(dict(x=P[0], w=P[1], bias=P[2], init=P[3], y=P[4], final=P[5]))
+    refused(_conv(lib, B=B, S=1, rows=B, D=1 << 17, **dict(conv, xs=1 << 17, ys=1 << 17)), words, code)
+    scan = _far(dict(x=P[0], dtp=P[1], A=P[2], Bm=P[3], Cm=P[4], skip=P[5], bias=P[6], z=P[7], h0=P[8], y=P[9],
+                     final=P[10], ws=P[11]))
+    refused(_scan(lib, B=B, S=1, rows=B, D=D, dts=D, zs=D, **wide, **scan, n=1 << 45), words, code)
