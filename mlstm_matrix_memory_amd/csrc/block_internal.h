@@ -148,6 +148,10 @@ struct Pieces {
     const int* seq_start;
     int B, S, rows, length, per;
     struct At { int b, c; };             // the c-th piece of sequence b
+    // Numbers in front of the first sequence's own, where rows lie before it, are no piece: c is
+    // then NONE, whose rows (c * length) are past every sequence's end, like those of numbers
+    // between two sequences.
+    static constexpr int NONE = 0x7fffffff;
     __host__ __device__ int count() const { return seq_start ? rows / length + B : B * per; }
     __device__ __forceinline__ int first(int b, const RowRange& sq) const {
         return seq_start ? sq.lo / length + b : b * per;
@@ -160,7 +164,8 @@ struct Pieces {
             if (min(max(seq_start[mid], 0), rows) / length + mid <= number) b = mid;
             else end = mid;
         }
-        return At{b, number - (min(max(seq_start[b], 0), rows) / length + b)};
+        const int c = number - (min(max(seq_start[b], 0), rows) / length + b);
+        return At{b, c < 0 ? NONE : c};
     }
     __device__ __forceinline__ RowRange sequence(int b) const { return sequence_rows(seq_start, b, S, rows); }
     // whether a sequence has the row
