@@ -465,7 +465,10 @@ mlstm_status mlstm_rms_norm_fwd(const void *x, long long x_stride,
  * The same with y in 8 bits: per row and group of `group` columns (32, 64 or 128;
  * 0 = the whole row; the last group may be shorter)
  *   scale = max |y| / 448,   q = e4m3(y / scale)   (round to nearest even)
- * and q = 0, scale = 0 where the group's y are all zero.
+ * of the fp32 y, scale and quotient (of scale before its rounding where that is below
+ * the smallest normal number), and q = 0, scale = 0 where the group's y are all zero.
+ * A NaN y has a NaN q and does not enter the maximum; where scale is infinite the
+ * finite y have q = 0 and the infinite ones NaN.
  *   q_out [rows,d] one OCP e4m3 byte per element, dense
  *   scale_out [rows, ceil(d/group)] fp32, dense
  */
