@@ -611,7 +611,8 @@ hipError_t bwd_t(const ScanArgs& a) {
     p.state = a.ws + f.state; p.before = a.ws + f.before; p.bc = a.ws + f.bc; p.sums = a.ws + f.sums;
     p.piece_h = a.ws + f.piece_h; p.piece_g = a.ws + f.piece_g; p.piece_s = a.ws + f.piece_s;
     const long long elems = (long long)a.rows * 2 * a.G * a.N, groups = (long long)scan_tiles(a.D, a.G) * f.pieces.count();
-    if (!launchable((elems + 255) / 256, 256)) return hipErrorInvalidConfiguration;
+    if (!launchable((elems + 255) / 256, 256) || !launchable((long long)((a.D + 63) / 64) * (a.N + 2), 1024))
+        return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)groups);
 #define SCAN_LAUNCH(NW, NL, CUT)                                                                               \
     hipLaunchKernelGGL((scan_bwd_states_kernel<T, NW, NL, CUT>), grid, dim3(64 * NW), 0, a.stream, p);         \

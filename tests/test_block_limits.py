@@ -1,0 +1,20 @@
+"""Limits of the block operators' entry points on the CPU: refusals that happen before any HIP
+call, what is accepted as far as the next check, and the words of the errors."""
+import pytest
+
+from mlstm_matrix_memory_amd import binding as b
+from test_block_abi import P, _far, _scan_bwd, refused
+
+
+def test_more_threads_than_the_parameter_sums_take():
+    """The backward's sums over the pieces run 1024 threads for every 64 channels and each of N + 2
+    gradients; past 2^32 of them nothing of the call is launched."""
+    b.load_library()
+    D, N = 1 << 23, 64
+    names = ("x", "dtp", "A", "Bm", "Cm", "skip", "bias", "z", "h0", "dy", "dh", "gx", "gdt", "gz", "gB", "gC", "gA", "gD",
+             "gb", "gh", "ws")
+    far = _far({k: P[i] for i, k in enumerate(names)})
+    wide = {k: D for k in ("xs", "dts", "zs", "ds", "gxs", "gdts", "gzs")}
+    narrow = {k: N for k in ("bs", "cs", "gBs", "gCs")}
+    status = _scan_bwd(b.load_library(), B=1, S=1, rows=1, D=D, N=N, n=1 << 45, **wide, **narrow, **far)
+    refused(status, "more threads than one launch takes", b.MLSTM_ERR_UNSUPPORTED)
