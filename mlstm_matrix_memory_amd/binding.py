@@ -141,13 +141,13 @@ def mlstm_error_detail() -> str:
     return load_library().mlstm_error_detail().decode()
 
 
-def _dtype_code(t) -> int:
+def _dtype_code(t, name: str = "q/k/v") -> int:
     import torch
     if t.dtype == torch.float32:
         return MLSTM_F32
     if t.dtype == torch.bfloat16:
         return MLSTM_BF16
-    raise TypeError(f"q/k/v must be float32 or bfloat16, got {t.dtype}")
+    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
 
 
 def mlstm_fwd_workspace_bytes(B: int, NH: int, S: int, d_qk: int, d_v: int, chunk: int, dtype: int) -> int:
@@ -696,11 +696,11 @@ def mlstm_rms_norm_bwd_workspace_bytes(rows: int, d: int) -> int:
 def _norm_inputs(x, weight, residual, residual_out, owned):
     import torch
     dev, d = _gpu(x, "x"), x.shape[-1]
-    _dtype_code(x)
+    _dtype_code(x, "x")
     _dense(weight, "weight", (d,), torch.float32, dev)
     res_dtype = x.dtype
     if residual is not None:
-        _dtype_code(residual)
+        _dtype_code(residual, "residual")
         res_dtype = residual.dtype
         _check_rows(residual, "residual", x.shape, res_dtype, dev)
         if residual_out is None:
@@ -710,7 +710,7 @@ def _norm_inputs(x, weight, residual, residual_out, owned):
         res_dtype = residual_out.dtype
     if residual_out is not None:
         _dense(residual_out, "residual_out", x.shape, res_dtype, dev)
-        _dtype_code(residual_out)
+        _dtype_code(residual_out, "residual_out")
     code = MLSTM_F32 if res_dtype == torch.float32 else MLSTM_BF16
     rows = x.numel() // d if d else 0
     return (x.data_ptr(), _row_stride(x, "x"), _ptr(residual),
@@ -733,7 +733,7 @@ def mlstm_rms_norm_fwd(x, weight, residual=None, eps: float = 1e-5, residual_out
     else:
         _dense(y_out, "y_out", x.shape, x.dtype, dev)
     _keep_for_stream(stream, dev, owned)
-    _launch("mlstm_rms_norm_fwd", dev, *head, float(eps), _dtype_code(x), res_code, _ptr(residual_out),
+    _launch("mlstm_rms_norm_fwd", dev, *head, float(eps), _dtype_code(x, "x"), res_code, _ptr(residual_out),
             y_out.data_ptr(), _raw_stream(stream, dev))
     return y_out, x if residual_out is None else residual_out
 
@@ -759,7 +759,7 @@ def mlstm_rms_norm_quant(x, weight, residual=None, eps: float = 1e-5, group: int
     _dense(q_out, "q_out", x.shape, torch.float8_e4m3fn, dev)
     _dense(scale_out, "scale_out", (*x.shape[:-1], per_row), torch.float32, dev)
     _keep_for_stream(stream, dev, owned)
-    _launch("mlstm_rms_norm_quant", dev, *head, float(eps), _dtype_code(x), res_code, group, _ptr(residual_out),
+    _launch("mlstm_rms_norm_quant", dev, *head, float(eps), _dtype_code(x, "x"), res_code, group, _ptr(residual_out),
             q_out.data_ptr(), scale_out.data_ptr(), _raw_stream(stream, dev))
     return q_out, scale_out, x if residual_out is None else residual_out
 
@@ -774,7 +774,7 @@ def mlstm_rms_norm_bwd(r, weight, dy, dres=None, eps: float = 1e-5, grad_x=None,
     """
     import torch
     dev, d = _gpu(r, "r"), r.shape[-1]
-    res_code, code = _dtype_code(r), _dtype_code(dy)
+    res_code, code = _dtype_code(r, "r"), _dtype_code(dy, "dy")
     _dense(weight, "weight", (d,), torch.float32, dev)
     _check_rows(dy, "dy", r.shape, dy.dtype, dev)
     if dres is not None:
@@ -832,7 +832,7 @@ def ssm_conv_fwd(x, weight, bias=None, act: int = SSM_ACT_SWISH, state_init=None
     [B,width-1,D] like x: the inputs before each sequence's first (None = zero).
     """
     import torch
-    dev, dt = _gpu(x, "x"), _dtype_code(x)
+    dev, dt = _gpu(x, "x"), _dtype_code(x, "x")
     B, S, rows = _batch(x, seq_start, max_len, dev)
     D, W = x.shape[-1], weight.shape[-1]
     _dense(weight, "weight", (D, W), torch.float32, dev)
@@ -855,7 +855,7 @@ def ssm_conv_step(x, weight, state, bias=None, act: int = SSM_ACT_SWISH, y_out=N
     """One row of the convolution per sequence: x [B,D]; state [B,width-1,D] is shifted
     in place.  Returns y [B,D]."""
     import torch
-    dev, dt = _gpu(x, "x"), _dtype_code(x)
+    dev, dt = _gpu(x, "x"), _dtype_code(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be 2-D [B, D]")
     (B, D), W = x.shape, weight.shape[-1]
@@ -884,7 +884,7 @@ def ssm_conv_bwd(x, weight, dy, bias=None, act: int = SSM_ACT_SWISH, state_init=
     gradients are float32; those of an absent bias or state_init are None.
     """
     import torch
-    dev, dt = _gpu(x, "x"), _dtype_code(x)
+    dev, dt = _gpu(x, "x"), _dtype_code(x, "x")
     B, S, rows = _batch(x, seq_start, max_len, dev)
     D, W = x.shape[-1], weight.shape[-1]
     _dense(weight, "weight", (D, W), torch.float32, dev)
@@ -945,7 +945,7 @@ def ssm_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = 
     dt_bias [D] float32; h_init and h_final [batch,D,N] float32 (None = zero).
     """
     import torch
-    dev, code = _gpu(x, "x"), _dtype_code(x)
+    dev, code = _gpu(x, "x"), _dtype_code(x, "x")
     batch, S, rows = _batch(x, seq_start, max_len, dev)
     args, width, G, N = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, batch, dev)
     if h_init is not None:
@@ -966,7 +966,7 @@ def ssm_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None, softplus: bool = T
     """One row of the scan per sequence: x, dt, z [batch,D], B, C [batch,G,N]; the state
     h [batch,D,N] float32 is updated in place.  Returns y [batch,D]."""
     import torch
-    dev, code = _gpu(x, "x"), _dtype_code(x)
+    dev, code = _gpu(x, "x"), _dtype_code(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be 2-D [batch, D]")
     batch = x.shape[0]
@@ -994,7 +994,7 @@ def ssm_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, softplus: boo
     others are float32; those of absent inputs are None.
     """
     import torch
-    dev, code = _gpu(x, "x"), _dtype_code(x)
+    dev, code = _gpu(x, "x"), _dtype_code(x, "x")
     batch, S, rows = _batch(x, seq_start, max_len, dev)
     args, width, G, N = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, batch, dev)
     _check_rows(dy, "dy", x.shape, x.dtype, dev)

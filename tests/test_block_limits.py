@@ -18,3 +18,25 @@ def test_more_threads_than_the_parameter_sums_take():
     narrow = {k: N for k in ("bs", "cs", "gBs", "gCs")}
     status = _scan_bwd(b.load_library(), B=1, S=1, rows=1, D=D, N=N, n=1 << 45, **wide, **narrow, **far)
     refused(status, "more threads than one launch takes", b.MLSTM_ERR_UNSUPPORTED)
+
+
+@pytest.mark.parametrize("name,call", [
+    ("x", lambda pkg, h, f: pkg.mlstm_rms_norm_fwd(h, f)),
+    ("x", lambda pkg, h, f: pkg.mlstm_rms_norm_quant(h, f)),
+    ("residual", lambda pkg, h, f: pkg.mlstm_rms_norm_fwd(h.float(), f, residual=h)),
+    ("residual_out", lambda pkg, h, f: pkg.mlstm_rms_norm_fwd(h.float(), f, residual_out=h)),
+    ("r", lambda pkg, h, f: pkg.mlstm_rms_norm_bwd(h, f, h.float())),
+    ("dy", lambda pkg, h, f: pkg.mlstm_rms_norm_bwd(h.float(), f, h)),
+    ("x", lambda pkg, h, f: pkg.ssm_conv_fwd(h, f)),
+    ("x", lambda pkg, h, f: pkg.ssm_conv_step(h, f, f)),
+    ("x", lambda pkg, h, f: pkg.ssm_conv_bwd(h, f, h)),
+    ("x", lambda pkg, h, f: pkg.ssm_scan_fwd(h, h, f, h, h)),
+    ("x", lambda pkg, h, f: pkg.ssm_step(h, h, f, h, h, f)),
+    ("x", lambda pkg, h, f: pkg.ssm_scan_bwd(h, h, f, h, h, h)),
+])
+def test_dtype_errors_name_their_tensor(name, call, monkeypatch):
+    import torch
+    import mlstm_matrix_memory_amd as pkg
+    monkeypatch.setattr(b, "_gpu", lambda t, _: t.device)
+    with pytest.raises(TypeError, match=f"^{name} must be float32 or bfloat16, got torch.float16"):
+        call(pkg, torch.zeros(2, 3, 8, dtype=torch.float16), torch.ones(8))
