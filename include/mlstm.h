@@ -427,7 +427,7 @@ mlstm_status slstm_fwd(const float *x_pre, const void *R, int B, int NH, int S, 
  *     at rows b*S .. b*S + S - 1 (rows = B*S).  With seq_start they are packed:
  *     seq_start[0..B] (int32, in device memory, ascending) gives sequence b the rows
  *     seq_start[b] .. seq_start[b+1] - 1 of `rows` rows, S is the length of the
- *     longest, and a sequence may be empty.  The kernels clamp the entries to
+ *     longest or a bound of it, at most rows, and a sequence may be empty.  The kernels clamp the entries to
  *     [0, rows] and a length to S, so no entry makes them leave the tensors; rows
  *     that belong to no sequence are neither read nor written.
  *   - Parameters, states and their gradients are fp32; gradients of activations have

@@ -807,7 +807,8 @@ SSM_ACT_SWISH = 1
 
 
 def _batch(x, seq_start, max_len, dev):
-    """(B, S, rows) of a batch: x [B, S, D], or packed sequences x [rows, D]."""
+    """(B, S, rows) of a batch: x [B, S, D], or packed sequences x [rows, D], of which max_len
+    bounds the lengths."""
     import torch
     if seq_start is None:
         if x.dim() != 3:
@@ -819,17 +820,18 @@ def _batch(x, seq_start, max_len, dev):
         raise ValueError("seq_start must be 1-D with a start per sequence and the last one's end")
     _dense(seq_start, "seq_start", (seq_start.numel(),), torch.int32, dev)
     if max_len is None:
-        raise ValueError("seq_start needs max_len, the length of the longest sequence")
-    return seq_start.numel() - 1, int(max_len), x.shape[0]
+        raise ValueError("seq_start needs max_len, the length of the longest sequence or a bound of it")
+    return seq_start.numel() - 1, min(int(max_len), x.shape[0]), x.shape[0]
 
 
 def ssm_conv_fwd(x, weight, bias=None, act: int = SSM_ACT_SWISH, state_init=None, seq_start=None, max_len=None,
                  y_out=None, state_final=None, stream=None):
     """Short causal depthwise convolution; returns (y, state_final).
 
-    x [B,S,D] (or packed [rows,D] with seq_start int32 [B+1] and max_len) float32 or
-    bfloat16; weight [D,width] and bias [D] float32, width 2 to 4; state_init
-    [B,width-1,D] like x: the inputs before each sequence's first (None = zero).
+    x [B,S,D] (or packed [rows,D] with seq_start int32 [B+1] and max_len, a bound of the
+    lengths) float32 or bfloat16; weight [D,width] and bias [D] float32, width 2 to 4;
+    state_init [B,width-1,D] like x: the inputs before each sequence's first (None = zero).
+    Rows of y that belong to no sequence are not written: undefined unless y_out is given.
     """
     import torch
     dev, dt = _gpu(x, "x"), _dtype_code(x, "x")
@@ -880,8 +882,9 @@ def ssm_conv_bwd(x, weight, dy, bias=None, act: int = SSM_ACT_SWISH, state_init=
     """Backward of ssm_conv_fwd; returns (grad_x, grad_weight, grad_bias, grad_state_init).
 
     Inputs as for the forward, dy like x, dstate_final like state_init.  grad_x is in
-    x's dtype (given, it may be a column range of a wider tensor), the parameters'
-    gradients are float32; those of an absent bias or state_init are None.
+    x's dtype (given, it may be a column range of a wider tensor; rows that belong to no
+    sequence are not written), the parameters' gradients are float32; those of an absent
+    bias or state_init are None.
     """
     import torch
     dev, dt = _gpu(x, "x"), _dtype_code(x, "x")
@@ -940,9 +943,10 @@ def ssm_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = 
                  max_len=None, y_out=None, h_final=None, workspace=None, stream=None):
     """Selective state space scan; returns (y, h_final).
 
-    x, dt, z [batch,S,D] (or packed [rows,D] with seq_start int32 [batch+1] and max_len)
-    and B, C [batch,S,G,N] in one dtype, float32 or bfloat16; A [D,N], D [D] and
-    dt_bias [D] float32; h_init and h_final [batch,D,N] float32 (None = zero).
+    x, dt, z [batch,S,D] (or packed [rows,D] with seq_start int32 [batch+1] and max_len, a
+    bound of the lengths) and B, C [batch,S,G,N] in one dtype, float32 or bfloat16; A [D,N],
+    D [D] and dt_bias [D] float32; h_init and h_final [batch,D,N] float32 (None = zero).
+    Rows of y that belong to no sequence are not written: undefined unless y_out is given.
     """
     import torch
     dev, code = _gpu(x, "x"), _dtype_code(x, "x")
@@ -990,8 +994,9 @@ def ssm_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, softplus: boo
     """Backward of ssm_scan_fwd; returns the gradients of (x, dt, A, B, C, D, z, dt_bias, h_init).
 
     Inputs as for the forward, dy like x, dh_final like h_init.  Gradients of x, dt, z, B
-    and C have their dtype (given, they may be column ranges of wider tensors), the
-    others are float32; those of absent inputs are None.
+    and C have their dtype (given, they may be column ranges of wider tensors; rows that
+    belong to no sequence are not written), the others are float32; those of absent inputs
+    are None.
     """
     import torch
     dev, code = _gpu(x, "x"), _dtype_code(x, "x")

@@ -40,3 +40,13 @@ def test_dtype_errors_name_their_tensor(name, call, monkeypatch):
     monkeypatch.setattr(b, "_gpu", lambda t, _: t.device)
     with pytest.raises(TypeError, match=f"^{name} must be float32 or bfloat16, got torch.float16"):
         call(pkg, torch.zeros(2, 3, 8, dtype=torch.float16), torch.ones(8))
+
+
+def test_max_len_is_any_bound_of_the_lengths():
+    """A caller may keep one bound for batches of any size: above the rows that there are it counts as these."""
+    import torch
+    x, start = torch.zeros(16, 8), torch.tensor([0, 5, 16], dtype=torch.int32)
+    assert b._batch(x, start, 4096, x.device) == (2, 16, 16)
+    assert b._batch(x, start, 11, x.device) == (2, 11, 16)
+    with pytest.raises(ValueError, match="max_len"):
+        b._batch(x, start, None, x.device)
