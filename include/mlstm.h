@@ -430,10 +430,15 @@ mlstm_status slstm_fwd(const float *x_pre, const void *R, int B, int NH, int S, 
  *     longest or a bound of it, at most rows, and a sequence may be empty.  The kernels clamp the entries to
  *     [0, rows] and a length to S, so no entry makes them leave the tensors; rows
  *     that belong to no sequence are neither read nor written.
- *   - Parameters, states and their gradients are fp32; gradients of activations have
- *     the activations' dtype (sums run in fp32 and are rounded once).
+ *   - Parameters, the scan's states and their gradients are fp32; the convolution's
+ *     states are past inputs and have their dtype; gradients of activations have the
+ *     activations' dtype (sums run in fp32 and are rounded once).
  *   - Outputs may not share bytes with inputs or each other except where said.
  *     Column ranges of one buffer with the same row stride do not count as sharing.
+ *   - NaN and infinities in the rows of a sequence reach what the formulas carry them
+ *     to: other sequences, and other channels but through sums over channels, keep
+ *     their values.  Where a formula gives an infinity the result may be NaN, and so may
+ *     every gradient of the parameters of a channel that meets one.
  *   - No atomics: repeated calls on the same inputs give the same bits.
  *   - At most 2^30 rows, 2^24 channels and 65535 sequences, and 2^32 - 1 threads in a
  *     launch; larger calls are MLSTM_ERR_UNSUPPORTED before anything is enqueued.
@@ -547,7 +552,8 @@ mlstm_status ssm_conv_bwd(const void *x, long long x_stride, const float *weight
  *   o_t  = sum_n C_t[g][n] h_t[n] + Dskip[d] x_t
  *   y_t  = o_t, or o_t z_t sigmoid(z_t) with z
  * softplus(v) = log(1 + e^v), taken as v above 20.  The state, the step size and all
- * sums are fp32.
+ * sums are fp32.  s A is meant to be <= 0; where it is positive, a product of decays
+ * that passes fp32's range makes the result NaN or infinite, also of a zero state.
  *   x, dt, z, y_out [rows,D] dtype (z NULL = no gate)
  *   A [D,N];  Dskip, dt_bias [D] or NULL (= 0)
  *   Bm, Cm [rows,G,N] dtype: element (row, g, n) at row*stride + g*N + n
