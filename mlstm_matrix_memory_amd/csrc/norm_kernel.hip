@@ -20,11 +20,11 @@ namespace {
 constexpr float E4M3_MAX = 448.0f;
 
 // y / scale, scale = m / 448, for a group whose largest |y| is m, rounded as a division rounds it: y
-// times the reciprocal, and the remainder of that times the reciprocal added.  (Without the remainder
-// one value in some hundred thousand lands on the neighbouring e4m3 step; the compiler's division costs
-// more: 8192 x 4096 in groups of 128 took 50 us without either, 51 us so and 55 us with a division.)  Small groups are scaled up, so that
-// the remainder keeps its bits, and so does a scale below the smallest normal number; groups of zeros
-// give zeros, and where scale is infinite finite values do.
+// times the reciprocal, and the remainder of that times the reciprocal added.  (Without the
+// remainder one value in some two million lands on the neighbouring e4m3 step; 8192 x 4096 in
+// groups of 128 took 50 us without it, 51 us so and 55 us with the compiler's division.)  Small
+// groups are scaled up, so that the remainder keeps its bits, and so does a scale below the
+// smallest normal number; groups of zeros give zeros, and where scale is infinite finite values do.
 struct Quotient {
     float up, scale, inv;
     __device__ __forceinline__ explicit Quotient(float m) {

@@ -8,10 +8,10 @@
 //   ds'_t (of the step size) = x_t du_t + sum_n A w_t
 //   dA = sum_t s_t w_t           dh_init = a_0 G_0
 // The states are needed in reverse order.  A first kernel runs forward and keeps one
-// state in every BWD_ROWS rows (4 bytes per state and BWD_ROWS rows through HBM, at N = 16 as
-// much as one fp32 activation); the second goes back over tiles of BWD_ROWS rows,
-// recomputes a tile's rows from the state in front of it and keeps their decays and
-// states in registers.  Arithmetic bounds both: per (row, channel, state) an exponential
+// state in every KEEP = 8 rows (4 bytes per state and 8 rows through HBM, at N = 16 as much as
+// two fp32 activations, written and read); the second goes back over tiles of BWD_ROWS = 16
+// rows, recomputes every 8 rows from the state in front of them and keeps their decays
+// and states in registers.  Arithmetic bounds both: per (row, channel, state) an exponential
 // and 3 vector instructions forward, twice, and about 11 back.
 //
 // In the second kernel a lane holds 4 states (or several times 4, one after the other)
@@ -48,7 +48,7 @@ struct BwdParams {
     void* dx; void* ddt; void* dz; void* dB; void* dC;
     long long dx_stride, ddt_stride, dz_stride, dB_stride, dC_stride;
     float* dA; float* dskip; float* dbias; float* dh_init;
-    float* state;                        // [slot][NP][D]: the state in front of each tile of rows
+    float* state;                        // [slot][NP][D]: the state in front of every KEEP rows
     float* before;                       // [slot][D]: sum of the step sizes from the piece's start to there
     float* bc;                           // [channel tile][row][2 NP]: its dB and dC
     float* sums;                         // [piece][NP + 2][D]: dA, dskip, dbias
@@ -56,8 +56,8 @@ struct BwdParams {
     float* piece_s;                      // [piece][D]: sum of the step sizes
 };
 
-// where a sequence's tiles of rows start among the slots of `state`: no two sequences share
-// one, and rows / KEEP + B slots hold them all
+// where a sequence's kept states start among the slots of `state`: no two sequences share a
+// slot, and rows / KEEP + B slots hold them all
 __device__ __forceinline__ int first_slot(const RowRange& sq, int b) { return sq.lo / KEEP + b; }
 
 // The piece, channel tile and rows of a workgroup, and its threads' part in staging
@@ -194,7 +194,7 @@ struct Work {
     }
 };
 
-// Forward over a piece: the states in front of its tiles of rows.  CUT: sequences have several
+// Forward over a piece: the states in front of every KEEP rows.  CUT: sequences have several
 // pieces; then also the sums of step sizes, the end state and R.
 template <typename T, int NW, int NL, bool CUT>
 __global__ __launch_bounds__(64 * NW) void scan_bwd_states_kernel(const BwdParams p)
@@ -543,10 +543,12 @@ __global__ __launch_bounds__(256) void scan_bwd_bc_kernel(const BwdParams p, int
 // 8.  The 6 lose because their workgroups fill the places 2.25 times: so the number is taken that
 // makes rounds * rows the least, with 24 rows for a piece's start, and among numbers within a
 // twentieth of that the largest.
-// The places by N: up to 8 states workgroups of one or two waves fit four times to a compute unit
-// ((1, 2048, 1536) at N = 4 took 111 us for 512 places and 76 us for 1024), above 16 their
-// registers leave room for one ((8, 1024, 2048) at N = 32 took 910 us in four pieces and
-// 784 us whole).
+// The places by N: up to 4 states a workgroup is one wave, four to a compute unit ((1, 2048, 1536)
+// at N = 4 took 111 us for 512 places and 76 us for 1024), above 16 registers leave room for
+// one workgroup ((8, 1024, 2048) at N = 32 took 910 us in four pieces and 784 us whole).  For 5
+// to 8 states, two waves whose registers leave room for two workgroups, neither count is the
+// better one: at N = 8, as 1024 and as 512 places, (1, 2048, 1536) took 108 and 99 us, (16, 1024,
+// 2048) 616 and 590, (2, 1024, 2048) 105 and 109, (24, 1024, 2048) 904 and 1017 us.
 constexpr int SHORTEST_PIECE = 48, START_ROWS = 24;
 int piece_rows(int S, int rows, int D, int G, int N) {
     const int places = N <= 8 ? 1024 : N <= 16 ? 512 : 256;
@@ -578,7 +580,7 @@ BwdPlan plan(const int* seq_start, int B, int S, int rows, int D, int G, int N) 
     f.cut = f.pieces.length < S;
     size_t at = 0;
     auto take = [&](size_t n) { const size_t o = at; at += (n + 63) / 64 * 64; return o; };
-    // as many tiles of rows and pieces as packed sequences may need (also where they are not
+    // as many kept states and pieces as packed sequences may need (also where they are not
     // packed: a workspace's size does not depend on seq_start)
     const size_t slots = (size_t)rows / KEEP + B, parts = (size_t)rows / f.pieces.length + B;
     f.state = take(slots * NP * D);

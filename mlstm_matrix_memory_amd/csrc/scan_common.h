@@ -1,12 +1,13 @@
-// Layout shared by the selective scan's forward and backward kernels.
+// Layout shared by the selective scan's kernels over sequences.
 //
-// A workgroup runs TILE = 64 neighbouring channels of one group, one channel per lane;
-// its NW waves share them and split the states, NL of the NP = NW * NL (>= N, the
-// states past N are zero) to each.  A lane then holds a channel's NL states in
-// registers and the recurrence needs no exchange between lanes.  B_t[n] and C_t[n]
-// are the same for all lanes of a wave: every 16 lanes hold NL of them, one per
-// lane, and the products read them through the DPP row broadcast, which costs no
-// instruction of its own.
+// A workgroup runs SCAN_TILE = 64 neighbouring channels of one group; its NW scanning waves
+// split the NP = NW * NL (>= N, the states past N are zero) states.  In the forward and
+// in the backward's first kernel a lane is a channel and a wave has NL of its states in
+// registers, so the recurrence needs no exchange between lanes.  B_t[n] is then the
+// same for all lanes of a wave: every 16 lanes hold NL of them, one per lane, and the
+// products read them through the DPP row broadcast, which costs no instruction of its own;
+// C_t[n] is read so in the backward's first kernel, and as vectors from LDS in the forward.
+// The backward's main kernel lays its states out otherwise (described there).
 #pragma once
 
 #include <utility>

@@ -413,8 +413,10 @@ hipError_t fwd_t(const ScanArgs& a) {
     p.y = a.y; p.h_final = a.h_final;
     p.piece_h = a.ws; p.piece_s = a.ws + f.state;
     const long long grid = (long long)scan_tiles(a.D, a.G) * f.pieces.count();
-    // Tiles of 32 rows have half the barriers but take 104 KB of LDS, one workgroup to a compute
-    // unit; of 16 rows three fit.  (4, 2048, 4096), 256 workgroups, uncut: 157 us against 177 us;
+    // Tiles of 32 rows have half the barriers but at N = 16 take 104 KB of LDS, one workgroup to a
+    // compute unit; of 16 rows two fit (by their 81 to 96 registers; by LDS three).  Uncut
+    // sequences of at most 4 states and more than 64 rows always have more than 256 workgroups,
+    // so the 32-row tiles of one wave run short ones only.  (4, 2048, 4096), 256 workgroups, uncut: 157 us against 177 us;
     // (16, 1024, 2048), 512 workgroups: 165 us against 139 us.
     const bool deep = !f.state && grid <= 256;
 #define SCAN_LAUNCH(NW, NL, ROWS, STATE, GATE) \
