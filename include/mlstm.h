@@ -630,8 +630,11 @@ mlstm_status mlstm_quant_e4m3(const void* x, long long x_stride, int rows, int c
  * Product of two e4m3 matrices with a scale for each block of 128:
  *   y[m][n] = sum over blocks j of a_scale[m][j] b_scale[n / block_rows][j]
  *                                  sum over k in block j of a[m][k] b[n][k]
- * The blocks are 128 columns, the last may be shorter.  All sums are fp32 (order: within a block
- * the matrix instruction's, then the blocks), rounded once to out_dtype.
+ * The blocks are 128 columns, the last may be shorter.  Sums are fp32 (order: within a block the
+ * matrix instruction's, then the blocks), rounded once to out_dtype.  But in bf16 results of M > 64 the
+ * e4m3 instruction cuts each of eight neighbouring terms (k = 8 i .. 8 i + 7) to a multiple of 2^-13 of the
+ * largest one's power of two before it adds them: at most 2^-10 of the largest term of each eight,
+ * less than the rounding of the result unless large terms cancel.  fp32 results have fp32 sums.
  *   a [M,K], b [N,K]: OCP e4m3 bytes, dense;  a_scale [M,ceil(K/128)] fp32, dense
  *   b_scale [ceil(N/block_rows),ceil(K/128)] fp32, dense;  block_rows 1 or 128
  *   y_out [M,N] out_dtype, rows y_stride elements apart

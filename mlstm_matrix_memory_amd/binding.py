@@ -1088,7 +1088,8 @@ def mlstm_mm_e4m3(a, a_scale, b, b_scale, block_rows: int = 128, out_dtype=None,
     a [..., K] torch.float8_e4m3fn with a_scale [..., ceil(K/128)] float32, b [N, K] with b_scale
     [ceil(N/block_rows), ceil(K/128)], block_rows 1 or 128, as mlstm_quant_e4m3 and
     mlstm_rms_norm_quant (group 128) give them.  out_dtype float32 or bfloat16 (the default, or
-    y_out's); y_out may be a column range of a wider tensor.
+    y_out's); y_out may be a column range of a wider tensor.  bfloat16 results of more than 64 rows are not
+    sums in fp32: each eight neighbouring terms lose up to 2^-10 of the largest of them.
     """
     import torch
     dev, block_rows = _gpu(a, "a"), int(block_rows)

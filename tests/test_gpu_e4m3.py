@@ -253,3 +253,52 @@ def test_captured_and_replayed():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, pair())
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("M,N,K", [(1, 20, 300), (16, 40, 256), (40, 33, 1000), (64, 50, 400), (65, 70, 400), (200, 140, 304), (130, 70, 301)])
+def test_terms_that_cancel(M, N, K, block_rows, out):
+    """Values of 14 powers of two whose second half of a block takes the first half back, but for its last eight.  fp32
+    sums in fp32 results and up to 64 rows; above that a bf16 result's eight neighbouring terms are each cut by less than 2^-13
+    of the largest one's power of two: 7 of them, as the largest is whole."""
+    import torch
+    from mlstm_matrix_memory_amd import mlstm_mm_e4m3
+    announce(f"mm of terms that cancel M={M} N={N} K={K} blocks of {block_rows} {out}")
+    rng = np.random.default_rng(M + N + K)
+    qa, qb = (e4m3(np.clip(rng.standard_normal((n, K)) * 2.0 ** rng.integers(-6, 8, K), -448, 448)) for n in (M, N))
+    for j in range(0, K - 127, BLOCK):
+        qa[:, j + 64:j + 120], qb[:, j + 64:j + 120] = qa[:, j:j + 56], -qb[:, j:j + 56]
+    blocks = -(-K // BLOCK)
+    sa, sb = (np.exp(rng.standard_normal((n, blocks))).astype(np.float32) for n in (M, -(-N // block_rows)))
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    y = mlstm_mm_e4m3(e4m3_gpu(qa), to_gpu(sa, "f32"), e4m3_gpu(qb), to_gpu(sb, "f32"), block_rows=block_rows, out_dtype=dt)
+    torch.cuda.synchronize()
+    r, bound = expected(qa, sa, qb, sb, block_rows, "f32")
+    if out == "bf16":
+        if M > 64:
+            wide = lambda x: np.pad(x, ((0, 0), (0, -K % 8))).reshape(len(x), -1, 8)  # noqa: E731
+            for i in range(0, -(-K // 8)):
+                a, b = wide(qa)[:, i], wide(qb)[:, i]
+                scale = sa[:, None, 8 * i // BLOCK] * np.repeat(sb, block_rows, 0)[None, :N, 8 * i // BLOCK].astype(np.float64)
+                bound = bound + 7 * 2.0 ** -13 * np.abs(a[:, None] * b[None]).max(2) * scale
+        bound = bound + 2.0 ** -8 * (np.abs(r) + bound)
+    ref.assert_within("y", to_np(y), r, bound)
+
+
+@pytest.mark.parametrize("M", [1, 16, 17, 33, 64])
+def test_small_terms_beside_two_that_cancel(M):
+    """126 equal terms beside 448^2 and -448^2, which the eight neighbours of one or of both must not lose."""
+    import torch
+    from mlstm_matrix_memory_amd import mlstm_mm_e4m3
+    announce(f"mm of small terms beside two large ones M={M}")
+    for small in (4.0, 1.0):
+        for first, second in ((0, 1), (0, 127), (3, 64)):
+            qa, qb = np.full((M, 128), small), np.ones((20, 128))
+            qa[:, [first, second]] = 448
+            qb[:, first], qb[:, second] = 448, -448
+            ones = lambda n: to_gpu(np.ones((n, 1)), "f32")  # noqa: E731
+            for dt in (torch.bfloat16, torch.float32):
+                y = to_np(mlstm_mm_e4m3(e4m3_gpu(qa), ones(M), e4m3_gpu(qb), ones(20), block_rows=1, out_dtype=dt))
+                bound = 129 * 2.0 ** -24 * (2 * 448.0 ** 2 + 126 * small)
+                ref.assert_within("y", y, np.full((M, 20), 126 * small), bound + (2.0 ** -8 * (126 * small + bound) if dt == torch.bfloat16 else 0))
