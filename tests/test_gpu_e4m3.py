@@ -302,3 +302,21 @@ def test_small_terms_beside_two_that_cancel(M):
                 y = to_np(mlstm_mm_e4m3(e4m3_gpu(qa), ones(M), e4m3_gpu(qb), ones(20), block_rows=1, out_dtype=dt))
                 bound = 129 * 2.0 ** -24 * (2 * 448.0 ** 2 + 126 * small)
                 ref.assert_within("y", y, np.full((M, 20), 126 * small), bound + (2.0 ** -8 * (126 * small + bound) if dt == torch.bfloat16 else 0))
+
+
+@pytest.mark.parametrize("M", [5, 70])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("a_size,b_size", [(-70, -50), (-110, 4), (100, -90), (60, 40), (-90, 100)])
+def test_scales_far_from_one(a_size, b_size, out, M):
+    """Scales whose products are normal numbers, and a block of zeros, whose scale is zero."""
+    import torch
+    from mlstm_matrix_memory_amd import mlstm_mm_e4m3
+    announce(f"mm with scales of 2^{a_size} and 2^{b_size} M={M} {out}")
+    qa, sa, qb, sb = operands(M, 140, 300, 128)
+    qa[:, 128:256], sa[:, 1] = 0, 0
+    sa, sb = sa * np.float32(2.0) ** a_size, sb * np.float32(2.0) ** b_size
+    dt = torch.bfloat16 if out == "bf16" else torch.float32
+    y = mlstm_mm_e4m3(e4m3_gpu(qa), to_gpu(sa, "f32"), e4m3_gpu(qb), to_gpu(sb, "f32"), out_dtype=dt)
+    torch.cuda.synchronize()
+    r, bound = expected(qa, sa, qb, sb, 128, out)
+    ref.assert_within("y", to_np(y), r, bound)
