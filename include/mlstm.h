@@ -662,13 +662,17 @@ mlstm_status mlstm_mm_e4m3(const void* a, const float* a_scale, const void* b, c
  *   h_final like it, or NULL (not wanted): the state after the last row (h_init's own, or zero,
  *   where a sequence is empty); may not be h_init's buffer
  *   H a multiple of G;  1 <= dk, dv <= 1024;  scale finite
- *   workspace: lin_attn_fwd_workspace_bytes(...) bytes, 16-byte aligned
+ *   workspace: lin_attn_fwd_workspace_bytes(...) bytes suffice for any call of the sizes;
+ *   lin_attn_fwd_call_workspace_bytes(...) are what one takes, with packed: seq_start is given, states: h_init is
+ *   (none for sequences of up to 128 rows without h_init; NULL then).  16-byte aligned
  * Chunks of 128 rows: the states that enter them are carried along the sequence in fp32 (in
  * segments where few heads leave the chip idle), kept in dtype, and all chunks' rows follow at
  * once.  In bf16 the kept states are rounded as operands, and nothing else before the result; h_final
  * is not made of rounded values.  A row's NaN and infinities do not reach earlier rows.
  */
 size_t lin_attn_fwd_workspace_bytes(int B, int S, int rows, int H, int G, int dk, int dv, mlstm_dtype dtype);
+size_t lin_attn_fwd_call_workspace_bytes(int B, int S, int rows, int H, int G, int dk, int dv, mlstm_dtype dtype,
+                                         int packed, int states);
 mlstm_status lin_attn_fwd(const void* q, long long q_stride, const void* k, long long k_stride,
                           const void* v, long long v_stride, const float* log_decay,
                           const int* seq_start, const float* h_init,
@@ -691,9 +695,11 @@ mlstm_status lin_attn_step(const void* q, long long q_stride, const void* k, lon
  *   grad_q, grad_k [rows,G,dk], grad_v [rows,H,dv] dtype, with their own strides; the heads of a
  *   group are summed in fp32
  *   grad_h_init [B,H,dv,dk] fp32, or NULL (not wanted)
- *   workspace: lin_attn_bwd_workspace_bytes(...) bytes, 16-byte aligned
+ *   workspace: as in the forward, with states: h_init or dh_final is given
  */
 size_t lin_attn_bwd_workspace_bytes(int B, int S, int rows, int H, int G, int dk, int dv, mlstm_dtype dtype);
+size_t lin_attn_bwd_call_workspace_bytes(int B, int S, int rows, int H, int G, int dk, int dv, mlstm_dtype dtype,
+                                         int packed, int states);
 mlstm_status lin_attn_bwd(const void* q, long long q_stride, const void* k, long long k_stride,
                           const void* v, long long v_stride, const float* log_decay,
                           const int* seq_start, const float* h_init,

@@ -75,8 +75,10 @@ from .binding import (  # noqa: F401
     ssm_scan_bwd,
     ssm_scan_bwd_workspace_bytes,
     lin_attn_bwd,
+    lin_attn_bwd_call_workspace_bytes,
     lin_attn_bwd_workspace_bytes,
     lin_attn_fwd,
+    lin_attn_fwd_call_workspace_bytes,
     lin_attn_fwd_workspace_bytes,
     lin_attn_step,
     mlstm_mm_e4m3,

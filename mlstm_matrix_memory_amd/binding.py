@@ -124,6 +124,9 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     for name in ("lin_attn_fwd_workspace_bytes", "lin_attn_bwd_workspace_bytes"):
         getattr(lib, name).restype = sz
         getattr(lib, name).argtypes = [i] * 8
+    for name in ("lin_attn_fwd_call_workspace_bytes", "lin_attn_bwd_call_workspace_bytes"):
+        getattr(lib, name).restype = sz
+        getattr(lib, name).argtypes = [i] * 10
     lib.lin_attn_fwd.restype = i
     lib.lin_attn_fwd.argtypes = [vp, ll, vp, ll, vp, ll, vp, vp, vp, i, i, i, i, i, i, i, f, i, vp, ll, vp, vp, sz, vp]
     lib.lin_attn_step.restype = i
@@ -1150,6 +1153,11 @@ def lin_attn_fwd_workspace_bytes(B: int, S: int, rows: int, H: int, G: int, dk: 
     return int(load_library().lin_attn_fwd_workspace_bytes(B, S, rows, H, G, dk, dv, int(dtype)))
 
 
+def lin_attn_fwd_call_workspace_bytes(B: int, S: int, rows: int, H: int, G: int, dk: int, dv: int, dtype: int, packed: bool,
+                                      states: bool) -> int:
+    return int(load_library().lin_attn_fwd_call_workspace_bytes(B, S, rows, H, G, dk, dv, int(dtype), int(packed), int(states)))
+
+
 def lin_attn_fwd(q, k, v, log_decay, scale=None, h_init=None, seq_start=None, max_len=None, o_out=None, h_final=None,
                  workspace=None, stream=None):
     """Linear attention with a decay for each head; returns (o, h_final).
@@ -1168,7 +1176,8 @@ def lin_attn_fwd(q, k, v, log_decay, scale=None, h_init=None, seq_start=None, ma
     o_out = _output(o_out, "o_out", v.shape, q.dtype, dev, owned)
     h_final = _output(h_final, "h_final", (B, H, dv, dk), torch.float32, dev, owned)
     _dense(h_final, "h_final", (B, H, dv, dk), torch.float32, dev)
-    ws, ws_bytes = _workspace(workspace, lin_attn_fwd_workspace_bytes(B, S, rows, H, G, dk, dv, code), dev, owned)
+    need = lin_attn_fwd_call_workspace_bytes(B, S, rows, H, G, dk, dv, code, seq_start is not None, h_init is not None)
+    ws, ws_bytes = _workspace(workspace, need, dev, owned)
     _keep_for_stream(stream, dev, owned)
     _launch("lin_attn_fwd", dev, *args, _ptr(seq_start), _ptr(h_init), B, S, rows, H, G, dk, dv,
             float(dk ** -0.5 if scale is None else scale), code, o_out.data_ptr(), _row_stride(o_out, "o_out", 2),
@@ -1195,6 +1204,11 @@ def lin_attn_bwd_workspace_bytes(B: int, S: int, rows: int, H: int, G: int, dk: 
     return int(load_library().lin_attn_bwd_workspace_bytes(B, S, rows, H, G, dk, dv, int(dtype)))
 
 
+def lin_attn_bwd_call_workspace_bytes(B: int, S: int, rows: int, H: int, G: int, dk: int, dv: int, dtype: int, packed: bool,
+                                      states: bool) -> int:
+    return int(load_library().lin_attn_bwd_call_workspace_bytes(B, S, rows, H, G, dk, dv, int(dtype), int(packed), int(states)))
+
+
 def lin_attn_bwd(q, k, v, log_decay, do, scale=None, h_init=None, seq_start=None, max_len=None, dh_final=None, grad_q=None,
                  grad_k=None, grad_v=None, workspace=None, stream=None):
     """Backward of lin_attn_fwd; returns the gradients of (q, k, v, h_init).
@@ -1216,7 +1230,9 @@ def lin_attn_bwd(q, k, v, log_decay, do, scale=None, h_init=None, seq_start=None
     grad_v = _output(grad_v, "grad_v", v.shape, q.dtype, dev, owned)
     grad_h = None if h_init is None else torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
     owned.append(grad_h)
-    ws, ws_bytes = _workspace(workspace, lin_attn_bwd_workspace_bytes(B, S, rows, H, G, dk, dv, code), dev, owned)
+    need = lin_attn_bwd_call_workspace_bytes(B, S, rows, H, G, dk, dv, code, seq_start is not None,
+                                             h_init is not None or dh_final is not None)
+    ws, ws_bytes = _workspace(workspace, need, dev, owned)
     _keep_for_stream(stream, dev, owned)
     _launch("lin_attn_bwd", dev, *args, _ptr(seq_start), _ptr(h_init), do.data_ptr(), _row_stride(do, "do", 2),
             _ptr(dh_final), B, S, rows, H, G, dk, dv, float(dk ** -0.5 if scale is None else scale), code,

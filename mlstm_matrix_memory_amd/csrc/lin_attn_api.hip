@@ -65,27 +65,38 @@ mlstm_status check_launches(const mlstm::LaBatch& b, int dk, int dv, bool heads)
 size_t whole16(size_t n) { return (n + 15) / 16 * 16; }
 
 // The kept states, then the segments' sums, then (backward, where heads share q and k) their gradients
-// by head.  Packed batches have room for the chunks and segments that any seq_start makes.
+// by head.  Packed batches have room for the chunks and segments that any seq_start makes.  Sequences of one chunk
+// with no state at an end that needs one keep none.
+bool keeps(int S, bool states) { return states || S > mlstm::LA_CHUNK; }
+
 struct Workspace { size_t kept, parts, heads, all; };
-Workspace workspace_of(const mlstm::LaBatch& b, int G, int dk, int dv, bool backward) {
+Workspace workspace_of(const mlstm::LaBatch& b, int G, int dk, int dv, bool keep, bool backward) {
     Workspace w = {};
-    w.kept = whole16(mlstm::la_kept_bytes(b, dk, dv));
-    w.parts = whole16(mlstm::la_state_parts_bytes(b, dk, dv));
+    w.kept = keep ? whole16(mlstm::la_kept_bytes(b, dk, dv)) : 0;
+    w.parts = keep ? whole16(mlstm::la_state_parts_bytes(b, dk, dv)) : 0;
     w.heads = backward && G < b.H ? whole16((size_t)b.rows * b.H * dk * 4) : 0;
     w.all = w.kept + w.parts + w.heads;
     return w;
 }
 
-size_t workspace_bytes_of(int B, int S, int rows, int H, int G, int dk, int dv, mlstm_dtype dt, bool backward) {
+// of a call of these sizes; 0 for sizes that are refused
+size_t call_bytes(int B, int S, int rows, int H, int G, int dk, int dv, mlstm_dtype dt, bool packed, bool states, bool backward) {
     if (check_heads(H, G, dk, dv) != MLSTM_OK || (dt != MLSTM_F32 && dt != MLSTM_BF16) || B < 1 || B > MAX_SEQUENCES ||
-        S < 1 || rows < 1 || rows > MAX_ROWS || S > rows)
+        S < 1 || rows < 1 || rows > MAX_ROWS || S > rows || (!packed && (long long)B * S != rows))
         return 0;
-    // what a packed batch takes, or one of equal sequences, whose pieces are numbered otherwise
     const int any = 0;
-    const size_t packed = workspace_of(make(B, S, rows, H, dt, &any), G, dk, dv, backward).all;
-    const size_t equal = (long long)B * S == rows ? workspace_of(make(B, S, rows, H, dt, nullptr), G, dk, dv, backward).all : 0;
+    return workspace_of(make(B, S, rows, H, dt, packed ? &any : nullptr), G, dk, dv, keeps(S, states), backward).all;
+}
+
+size_t workspace_bytes_of(int B, int S, int rows, int H, int G, int dk, int dv, mlstm_dtype dt, bool backward) {
+    // what a packed batch takes, or one of equal sequences, whose pieces are numbered otherwise
+    const size_t packed = call_bytes(B, S, rows, H, G, dk, dv, dt, true, true, backward);
+    const size_t equal = call_bytes(B, S, rows, H, G, dk, dv, dt, false, true, backward);
     return packed > equal ? packed : equal;
 }
+
+// the workspace as a tensor of the call, absent where it takes none
+Region workspace_region(void* ws, size_t bytes) { return dense(bytes ? ws : nullptr, bytes, 1, "workspace", true, true); }
 
 }  // namespace
 
@@ -93,6 +104,11 @@ extern "C" {
 
 size_t lin_attn_fwd_workspace_bytes(int B, int S, int rows, int H, int G, int dk, int dv, mlstm_dtype dt) {
     return workspace_bytes_of(B, S, rows, H, G, dk, dv, dt, false);
+}
+
+size_t lin_attn_fwd_call_workspace_bytes(int B, int S, int rows, int H, int G, int dk, int dv, mlstm_dtype dt, int packed,
+                                         int states) {
+    return call_bytes(B, S, rows, H, G, dk, dv, dt, packed != 0, states != 0, false);
 }
 
 mlstm_status lin_attn_fwd(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
@@ -105,16 +121,15 @@ mlstm_status lin_attn_fwd(const void* q, long long q_stride, const void* k, long
     MLSTM_TRY(check_inputs(in, r));
     const mlstm::LaBatch b = make(in);
     MLSTM_TRY(check_launches(b, dk, dv, false));
-    const Workspace w = workspace_of(b, G, dk, dv, false);
+    const bool keep = keeps(S, h_init != nullptr);
+    const Workspace w = workspace_of(b, G, dk, dv, keep, false);
     MLSTM_TRY(workspace(ws, workspace_bytes, w.all, 16));
     r[INPUTS] = strided(o_out, rows, (size_t)H * dv, o_stride, elem(dt), "o_out", true);
     r[INPUTS + 1] = dense(h_final, (size_t)B * H * dv * dk, 4, "h_final", true, true);
-    r[INPUTS + 2] = dense(ws, w.all, 1, "workspace", true);
+    r[INPUTS + 2] = workspace_region(ws, w.all);
     MLSTM_TRY(regions(r, INPUTS + 3));
     MLSTM_TRY(disjoint(r, INPUTS + 3));
     const mlstm::LaRows qr = {q, q_stride, dk, H / G}, kr = {k, k_stride, dk, H / G}, vr = {v, v_stride, dv, 1};
-    // sequences of one chunk without a state at their start need none kept
-    const bool keep = h_init || S > mlstm::LA_CHUNK;
     if (keep || h_final) {
         mlstm::LaStates s = {};
         s.x = vr; s.y = kr; s.init = h_init; s.final = h_final; s.kept = keep ? ws : nullptr; s.parts = (float*)((char*)ws + w.kept);
@@ -148,6 +163,11 @@ size_t lin_attn_bwd_workspace_bytes(int B, int S, int rows, int H, int G, int dk
     return workspace_bytes_of(B, S, rows, H, G, dk, dv, dt, true);
 }
 
+size_t lin_attn_bwd_call_workspace_bytes(int B, int S, int rows, int H, int G, int dk, int dv, mlstm_dtype dt, int packed,
+                                         int states) {
+    return call_bytes(B, S, rows, H, G, dk, dv, dt, packed != 0, states != 0, true);
+}
+
 mlstm_status lin_attn_bwd(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
                           long long v_stride, const float* log_decay, const int* seq_start, const float* h_init,
                           const void* dout, long long do_stride, const float* dh_final,
@@ -162,7 +182,7 @@ mlstm_status lin_attn_bwd(const void* q, long long q_stride, const void* k, long
     MLSTM_TRY(check_inputs(in, r));
     const mlstm::LaBatch b = make(in);
     MLSTM_TRY(check_launches(b, dk, dv, G < H));
-    const Workspace w = workspace_of(b, G, dk, dv, true);
+    const Workspace w = workspace_of(b, G, dk, dv, keeps(S, h_init || dh_final), true);
     MLSTM_TRY(workspace(ws, workspace_bytes, w.all, 16));
     const size_t el = elem(dt), kw = (size_t)G * dk, vw = (size_t)H * dv, state = (size_t)B * H * dv * dk;
     const Region more[COUNT - INPUTS] = {
@@ -172,7 +192,7 @@ mlstm_status lin_attn_bwd(const void* q, long long q_stride, const void* k, long
         strided(grad_k, rows, kw, grad_k_stride, el, "grad_k", true),
         strided(grad_v, rows, vw, grad_v_stride, el, "grad_v", true),
         dense(grad_h_init, state, 4, "grad_h_init", true, true),
-        dense(ws, w.all, 1, "workspace", true),
+        workspace_region(ws, w.all),
     };
     for (int n = 0; n < COUNT - INPUTS; ++n) r[INPUTS + n] = more[n];
     MLSTM_TRY(regions(r, COUNT));

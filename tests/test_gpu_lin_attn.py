@@ -232,3 +232,28 @@ def test_segments_of_wide_states(dtype):
     announce(f"lin_attn segments of wide states {dtype}")
     check(la.make(1, 1100, 1, 1, 72, 200, dtype, seed=70))
     check(la.make(1, 1050, 1, 1, 136, 264, dtype, seed=71, init=False))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_short_sequences_take_no_workspace(packed, dtype):
+    """Sequences of one chunk without states: the wrappers allocate their outputs and, where heads share q and k, the
+    gradients by head; results as ever."""
+    import torch
+    from mlstm_matrix_memory_amd import lin_attn_bwd, lin_attn_fwd
+    announce(f"lin_attn of short sequences without a workspace packed={packed} {dtype}")
+    for G in (4, 2):
+        c = la.make(5, 128, 4, G, 24, 40, dtype, seed=80 + G, init=False, lengths=[128, 0, 1, 77, 128] if packed else None)
+        check(c, packed)
+        t = on_gpu(c, packed)
+        t = {n: x.contiguous() if n in ("q", "k", "v", "do") else x for n, x in t.items()}
+        outputs = c["v"].size * t["v"].element_size() + 5 * 4 * 40 * 24 * 4
+        grads = (2 * c["q"].size + c["v"].size) * t["v"].element_size() + (0 if G == 4 else c["rows"] * 4 * 24 * 4)
+        for f, need in ((lambda: lin_attn_fwd(t["q"], t["k"], t["v"], t["g"], **t["plan"]), outputs),
+                        (lambda: lin_attn_bwd(t["q"], t["k"], t["v"], t["g"], t["do"], **t["plan"]), grads)):
+            torch.cuda.synchronize()
+            torch.cuda.reset_peak_memory_stats()
+            before = torch.cuda.memory_allocated()
+            f()
+            assert torch.cuda.max_memory_allocated() - before <= need + 4 * 512  # (allocations are whole 512 bytes)
+        torch.cuda.synchronize()

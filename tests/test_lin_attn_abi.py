@@ -113,3 +113,37 @@ def test_python_checks():
     for f, a in ((lin_attn_fwd, (q, q, v, g)), (lin_attn_step, (q, q, v, g, q)), (lin_attn_bwd, (q, q, v, g, v))):
         with pytest.raises(ValueError, match="GPU"):
             f(*a)
+
+
+def test_calls_that_keep_no_states_need_no_workspace_for_them(lib):
+    """Sequences of one chunk without a state at their start (in the backward: at either end) keep none: the
+    call goes on to its next check with no workspace, or with that of the gradients by head alone."""
+    short = dict(S=100, rows=200, h=None, ws=None, wb=0)
+    refused(_fwd(lib, **short, o=None), "o_out is NULL")
+    refused(_fwd(lib, **dict(short, S=128, rows=256), o=None), "o_out is NULL")
+    refused(_fwd(lib, **dict(short, S=129, rows=258)), "workspace of 0", b.MLSTM_ERR_WORKSPACE)
+    refused(_fwd(lib, **dict(short, h=P[4])), "workspace of 0", b.MLSTM_ERR_WORKSPACE)
+    back = dict(short, dhf=None, gq=None)
+    refused(_bwd(lib, **back), "workspace of 0", b.MLSTM_ERR_WORKSPACE)              # two heads share q and k
+    refused(_bwd(lib, **dict(back, ws=P[7], wb=200 * 4 * 32 * 4)), "grad_q is NULL")
+    refused(_bwd(lib, **dict(back, G=4, qs=128, ks=128)), "grad_q is NULL")
+    for one in (dict(h=P[4]), dict(dhf=P[6])):
+        refused(_bwd(lib, **dict(back, G=4, qs=128, ks=128, **one)), "workspace of 0", b.MLSTM_ERR_WORKSPACE)
+
+
+def test_workspace_bytes_of_a_call(lib):
+    """What one call takes, by whether it is packed and has states at its ends; the plain query is the largest of them."""
+    from mlstm_matrix_memory_amd import lin_attn_bwd_call_workspace_bytes, lin_attn_fwd_call_workspace_bytes
+    f, g = lin_attn_fwd_call_workspace_bytes, lin_attn_bwd_call_workspace_bytes
+    state = 64 * 64 * 2
+    assert f(2, 100, 200, 4, 2, 32, 48, 1, False, False) == 0 and f(2, 100, 200, 4, 2, 32, 48, 1, True, False) == 0
+    assert f(2, 100, 200, 4, 2, 32, 48, 1, False, True) == 2 * 4 * state and f(2, 100, 200, 4, 2, 32, 48, 1, True, True) == 3 * 4 * state
+    assert f(2, 130, 260, 4, 2, 32, 48, 1, False, False) == f(2, 130, 260, 4, 2, 32, 48, 1, False, True) == 4 * 4 * state
+    assert g(2, 100, 200, 4, 4, 32, 48, 1, False, False) == 0 and g(2, 100, 200, 4, 2, 32, 48, 1, False, False) == 200 * 4 * 32 * 4
+    assert g(2, 100, 200, 4, 4, 32, 48, 1, False, True) == 2 * 4 * state
+    for call, most in ((f, lib.lin_attn_fwd_workspace_bytes), (g, lib.lin_attn_bwd_workspace_bytes)):
+        for sizes in ((2, 100, 200, 4, 2, 32, 48, 1), (1, 5000, 5000, 2, 1, 40, 40, 0), (9, 700, 6300, 3, 3, 130, 70, 1)):
+            assert most(*sizes) == max(call(*sizes, packed, states) for packed in (False, True) for states in (False, True))
+    # sizes that make no batch
+    assert f(2, 100, 201, 4, 2, 32, 48, 1, False, True) == 0 and f(2, 100, 200, 4, 3, 32, 48, 1, True, True) == 0
+    assert g(0, 100, 200, 4, 2, 32, 48, 1, True, True) == 0
