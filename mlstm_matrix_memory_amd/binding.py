@@ -147,7 +147,7 @@ def header_symbols(path: str = HEADER) -> list[str]:
     """Names of the functions include/mlstm.h declares."""
     text = open(path).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return sorted(set(re.findall(r"\b((?:mlstm|slstm|ssm)_[a-z_0-9]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b((?:mlstm|slstm|ssm|lin_attn)_[a-z_0-9]+)\s*\(", text)))
 
 
 def mlstm_status_string(status: int) -> str:

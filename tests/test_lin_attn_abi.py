@@ -147,3 +147,16 @@ def test_workspace_bytes_of_a_call(lib):
     # sizes that make no batch
     assert f(2, 100, 201, 4, 2, 32, 48, 1, False, True) == 0 and f(2, 100, 200, 4, 3, 32, 48, 1, True, True) == 0
     assert g(0, 100, 200, 4, 2, 32, 48, 1, True, True) == 0
+
+
+def test_declared_exported_and_in_the_package(lib):
+    """The header's functions of these operators are among those that the export check goes through."""
+    import mlstm_matrix_memory_amd as pkg
+    names = b.header_symbols()
+    for name in ("lin_attn_fwd", "lin_attn_step", "lin_attn_bwd", "lin_attn_fwd_workspace_bytes", "lin_attn_bwd_workspace_bytes",
+                 "lin_attn_fwd_call_workspace_bytes", "lin_attn_bwd_call_workspace_bytes", "mlstm_quant_e4m3", "mlstm_mm_e4m3"):
+        assert name in names and hasattr(lib, name) and callable(getattr(pkg, name))
+    # every function that the header declares, whatever its prefix, is one of them
+    import re
+    text = re.sub(r"/\*.*?\*/", "", open(b.HEADER).read(), flags=re.S)
+    assert set(re.findall(r"^(?:mlstm_status|size_t|const char *\*) *(\w+)\s*\(", text, flags=re.M)) <= set(names)
