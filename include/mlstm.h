@@ -656,8 +656,8 @@ mlstm_status mlstm_mm_e4m3(const void* a, const float* a_scale, const void* b, c
  * a sequence, with the state S [dv,dk]:
  *   S_t = e^{log_decay} S_{t-1} + v_t k_t^T,    o_t = scale S_t q_t
  *   q, k [rows,G,dk], v, o_out [rows,H,dv] dtype: element (row, head, i) at row*stride + head*d + i
- *   log_decay [H]: <= 0 (minus infinity keeps nothing).  Where it is positive, powers that pass
- *   fp32's range make the result NaN or infinite.  It is a constant: no gradient is taken
+ *   log_decay [H]: <= 0 (minus infinity keeps nothing).  Results of a positive one may be NaN, also in
+ *   short sequences, once its power over 128 rows passes fp32's range.  It is a constant: no gradient is taken
  *   h_init [B,H,dv,dk] fp32 or NULL (= 0): the state that enters row 0
  *   h_final like it, or NULL (not wanted): the state after the last row (h_init's own, or zero,
  *   where a sequence is empty); may not be h_init's buffer
