@@ -468,8 +468,11 @@ hipError_t tile_pick(const MmArgs& a, const MmShape& s) {
     if (!aligned)
         return tiles128 >= 256 ? tile_launch<T, 2, 2, 4, 4, BLOCK, false>(a, s) : tile_launch<T, 2, 2, 2, 2, BLOCK, false>(a, s);
     // 256 x 256 where that fills the chip (8192 x 8192 x 2048: 186 us, with 128 x 128 209), 64 x 64 where 128 x 128 does not
-    const long long tiles256 = (long long)((a.M + 255) / 256) * ((a.N + 255) / 256);
-    if (sizeof(T) == 2 && tiles256 >= 256) return tile_launch<T, 4, 2, 4, 8, BLOCK, true>(a, s);
+    // (fp32 results keep to 128 x 128: their widened operands do not fit beside 256 x 256 accumulators)
+    if constexpr (sizeof(T) == 2) {
+        const long long tiles256 = (long long)((a.M + 255) / 256) * ((a.N + 255) / 256);
+        if (tiles256 >= 256) return tile_launch<T, 4, 2, 4, 8, BLOCK, true>(a, s);
+    }
     return tiles128 >= 256 ? tile_launch<T, 2, 2, 4, 4, BLOCK, true>(a, s) : tile_launch<T, 2, 2, 2, 2, BLOCK, true>(a, s);
 }
 
