@@ -322,12 +322,22 @@ def test_scales_far_from_one(a_size, b_size, out, M):
     ref.assert_within("y", to_np(y), r, bound)
 
 
+def expected_of_cut_terms(qa, sa, qb, sb, block_rows):
+    """(y, bound) of bf16 results of more than 64 rows: cut terms as in test_terms_that_cancel, the largest of eight being at
+    most the largest factors' product."""
+    K = qa.shape[1]
+    r, bound = expected(qa, sa, qb, sb, block_rows, "f32")
+    most = lambda q, s, rows: np.maximum.reduceat(np.abs(q), np.arange(0, K, 8), 1) * np.repeat(  # noqa: E731
+        np.repeat(s.astype(np.float64), rows, 0)[:len(q)], 16, 1)[:, :-(-K // 8)]
+    bound = bound + 7 * 2.0 ** -13 * most(qa, sa, 1) @ most(qb, sb, block_rows).T
+    return r, bound + 2.0 ** -8 * (np.abs(r) + bound)
+
+
 @pytest.mark.parametrize("block_rows", [1, 128])
 @pytest.mark.parametrize("M,N,K", [(4100, 4090, 528), (4096, 4100, 640), (2048, 2100, 656)])
 def test_product_of_several_blocks_in_large_tiles(M, N, K, block_rows):
     """256 x 256 and 128 x 128 tiles over five and six blocks, the last whole or shorter: both LDS buffers filled again
-    and again beside the products, with other scales in every block.  Cut terms as in test_terms_that_cancel, the
-    largest of eight being at most the largest factors' product."""
+    and again beside the products, with other scales in every block."""
     import torch
     from mlstm_matrix_memory_amd import mlstm_mm_e4m3
     announce(f"mm of several blocks M={M} N={N} K={K} blocks of {block_rows}")
@@ -336,8 +346,4 @@ def test_product_of_several_blocks_in_large_tiles(M, N, K, block_rows):
     sa, sb = ((s * np.exp2(rng.integers(-4, 5, s.shape))).astype(np.float32) for s in (sa, sb))
     y = mlstm_mm_e4m3(e4m3_gpu(qa), to_gpu(sa, "f32"), e4m3_gpu(qb), to_gpu(sb, "f32"), block_rows=block_rows)
     torch.cuda.synchronize()
-    r, bound = expected(qa, sa, qb, sb, block_rows, "f32")
-    most = lambda q, s, rows: np.maximum.reduceat(np.abs(q), np.arange(0, K, 8), 1) * np.repeat(  # noqa: E731
-        np.repeat(s.astype(np.float64), rows, 0)[:len(q)], 16, 1)[:, :K // 8]
-    bound = bound + 7 * 2.0 ** -13 * most(qa, sa, 1) @ most(qb, sb, block_rows).T
-    ref.assert_within("y", to_np(y), r, bound + 2.0 ** -8 * (np.abs(r) + bound))
+    ref.assert_within("y", to_np(y), *expected_of_cut_terms(qa, sa, qb, sb, block_rows))

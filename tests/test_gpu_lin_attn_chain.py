@@ -213,3 +213,61 @@ def test_widths_whose_rows_are_far_apart():
     want = la.reference(c)
     ref.assert_within("o", to_np(o).reshape(c["v"].shape), *want["o"])
     ref.assert_within("h", to_np(h), *want["h_final"])
+
+
+@pytest.mark.parametrize("rows", [140, 1])
+def test_every_stage_of_a_block(rows):
+    """The block's five calls over a prompt of two sequences, or (rows = 1) one row each after it: every stage against 64 bits
+    from the values that entered it."""
+    import torch
+    import mlstm_matrix_memory_amd as m
+    from test_gpu_e4m3 import expected, expected_of_cut_terms, quantised
+    announce(f"chain: every stage, rows={rows}")
+    p = _weights()
+    step, flat = rows == 1, lambda t: to_np(t).reshape(2 * rows, -1)  # noqa: E731
+    x = _normal((2, 256) if step else (2, rows, 256), 300 + rows)
+    g = to_np(p["g"]).astype(np.float32)
+    h = _normal((2, 4, 64, 48), 301, dtype=torch.float32) if step else None
+    before = None if h is None else to_np(h).astype(np.float32)
+    for (w, s), raw in ((p["w_in"], _normal((448, 256), 1, 256 ** -0.5)), (p["w_out"], _normal((256, 256), 2, 256 ** -0.5))):
+        q, scale, _ = quantised(to_np(raw), 128)
+        assert np.array_equal(to_np(w), q) and np.array_equal(to_np(s), scale)
+
+    q8, s8, _ = m.mlstm_rms_norm_quant(x, p["norm"], group=128)
+    proj = m.mlstm_mm_e4m3(q8, s8, *p["w_in"])
+    q, k, v = proj.split([96, 96, 256], -1)
+    heads = q.unflatten(-1, (2, 48)), k.unflatten(-1, (2, 48)), v.unflatten(-1, (4, 64)), p["g"]
+    if step:
+        o = m.lin_attn_step(*heads, h)
+    else:
+        o, h = m.lin_attn_fwd(*heads)
+    o8, os8 = m.mlstm_quant_e4m3(o.flatten(-2))
+    y = m.mlstm_mm_e4m3(o8, os8, *p["w_out"])
+    torch.cuda.synchronize()
+
+    # the norm: fp32's 1 / sqrt is 140 steps off at most (256 squares, half of whose sum's error is the root's, and 12 more
+    # roundings); e4m3 rounds by 2^-4 of a value or half its smallest step
+    r = ref.norm_fwd(ref.norm_sum(to_np(x).reshape(-1, 256), None, "f32"), np.ones(256), 1e-5)
+    scale = np.abs(r).reshape(-1, 2, 128).max(2) / 448
+    ref.assert_within("norm scale", flat(s8), scale, 140 * ref.U * scale)
+    wide = np.repeat(scale, 128, 1)
+    ref.assert_within("norm", flat(q8) * np.repeat(flat(s8), 128, 1), r, (1 + 1e-4) * np.maximum(2.0 ** -4 * np.abs(r), 2.0 ** -10 * wide))
+
+    def product(a, b):
+        """(y, bound) of a bf16 product; few rows sum in fp32."""
+        if not step:
+            return expected_of_cut_terms(*map(flat, a), *map(to_np, b), 128)
+        value, bound = expected(*map(flat, a), *map(to_np, b), 128, "f32")
+        return value, bound + 2.0 ** -8 * (np.abs(value) + bound)
+    ref.assert_within("projection", flat(proj), *product((q8, s8), p["w_in"]))
+    # the cell
+    at = flat(proj)
+    c = dict(q=at[:, :96].reshape(-1, 2, 48), k=at[:, 96:192].reshape(-1, 2, 48), v=at[:, 192:].reshape(-1, 4, 64), h=before, do=None,
+             dh=None, g=g, spans=[(0, rows), (rows, 2 * rows)], B=2, S=rows, rows=2 * rows, dtype="bf16", scale=48 ** -0.5)
+    want = la.reference(c)
+    ref.assert_within("o", flat(o).reshape(-1, 4, 64), *want["o"])
+    ref.assert_within("h", to_np(h), *want["h_final"])
+    # its quantiser, whole values, and the product back
+    value, scale, _ = quantised(flat(o), 1)
+    assert np.array_equal(flat(o8), value) and np.array_equal(flat(os8), scale)
+    ref.assert_within("y", flat(y), *product((o8, os8), p["w_out"]))
