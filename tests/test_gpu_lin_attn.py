@@ -257,3 +257,48 @@ def test_short_sequences_take_no_workspace(packed, dtype):
             f()
             assert torch.cuda.max_memory_allocated() - before <= need + 4 * 512  # (allocations are whole 512 bytes)
         torch.cuda.synchronize()
+
+
+def in_c(c, final=True, grad_h=True):
+    """A case through the C entry points: h_final NULL unless `final`, grad_h_init NULL unless `grad_h`, whatever h_init is."""
+    import torch
+    from mlstm_matrix_memory_amd import MLSTM_BF16, MLSTM_F32, binding
+    lib, t = binding.load_library(), on_gpu(c, False)
+    B, S, H, G, dk, dv = c["B"], c["S"], c["v"].shape[1], c["q"].shape[1], c["q"].shape[2], c["v"].shape[2]
+    code, f32 = (MLSTM_BF16 if c["dtype"] == "bf16" else MLSTM_F32), dict(dtype=torch.float32, device="cuda")
+    row, ptr = t["q"].stride(1), lambda x: None if x is None else x.data_ptr()  # noqa: E731
+    head = [y for n in ("q", "k", "v") for y in (ptr(t[n]), row)] + [ptr(t["g"]), None, ptr(t["h"])]
+    sizes = [B, S, B * S, H, G, dk, dv, c["scale"], code]
+    bytes_of = lambda f, states: f(B, S, B * S, H, G, dk, dv, code, 0, states)  # noqa: E731
+    need = [bytes_of(lib.lin_attn_fwd_call_workspace_bytes, int(c["h"] is not None)),
+            bytes_of(lib.lin_attn_bwd_call_workspace_bytes, int(c["h"] is not None or c["dh"] is not None))]
+    ws = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") if n else None for n in need]
+    o, gv = (torch.empty(B, S, H, dv, dtype=t["v"].dtype, device="cuda") for _ in range(2))
+    gq, gk = (torch.empty(B, S, G, dk, dtype=t["v"].dtype, device="cuda") for _ in range(2))
+    h_final, gh = (torch.empty(B, H, dv, dk, **f32) if wanted else None for wanted in (final, grad_h))
+    stream = torch.cuda.current_stream().cuda_stream
+    st = lib.lin_attn_fwd(*head, *sizes, ptr(o), H * dv, ptr(h_final), ptr(ws[0]), need[0], stream)
+    assert st == 0, binding.mlstm_error_detail()
+    st = lib.lin_attn_bwd(*head, ptr(t["do"]), row, ptr(t["dh"]), *sizes, ptr(gq), G * dk, ptr(gk), G * dk, ptr(gv), H * dv, ptr(gh),
+                          ptr(ws[1]), need[1], stream)
+    assert st == 0, binding.mlstm_error_detail()
+    torch.cuda.synchronize()
+    like = {"o": c["v"], "dq": c["q"], "dk": c["q"], "dv": c["v"]}
+    got = {"o": o, "dq": gq, "dk": gk, "dv": gv, "h_final": h_final, "dh0": gh}
+    return {n: to_np(x).reshape(like[n].shape) if n in like else to_np(x) for n, x in got.items() if x is not None}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("S", [100, 300, 1100])
+@pytest.mark.parametrize("final,h,dh,grad_h", [(False, True, True, True), (False, False, False, False), (True, True, True, False),
+                                               (True, False, True, True), (False, False, False, True), (False, True, False, False)])
+def test_final_states_and_gradients_that_are_not_wanted(final, h, dh, grad_h, S, dtype):
+    """The C entry points without h_final, without grad_h_init though there is an h_init, with it though there is none; in
+    one chunk, in several, in segments, from workspaces of exactly the call's bytes that hold NaN."""
+    announce(f"lin_attn in C final={final} h={h} dh={dh} grad_h={grad_h} S={S} {dtype}")
+    c = la.make(1, S, 2, 1, 24, 40, dtype, seed=90 + S)
+    want_of = dict(c, h=c["h"] if h else None, dh=c["dh"] if dh else None)
+    got, want = in_c(want_of, final, grad_h), la.reference(want_of)
+    assert ("h_final" in got) == final and ("dh0" in got) == grad_h
+    for n, x in got.items():
+        ref.assert_within(n, x, *want[n])
