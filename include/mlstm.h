@@ -667,8 +667,10 @@ mlstm_status mlstm_mm_e4m3(const void* a, const float* a_scale, const void* b, c
  *   (none for sequences of up to 128 rows without h_init; NULL then).  16-byte aligned
  * Chunks of 128 rows: the states that enter them are carried along the sequence in fp32 (in
  * segments where few heads leave the chip idle), kept in dtype, and all chunks' rows follow at
- * once.  In bf16 the kept states are rounded as operands, and nothing else before the result; h_final
- * is not made of rounded values.  A row's NaN and infinities do not reach earlier rows.
+ * once.  In bf16 the kept states are rounded as operands (by 2^-8 at most); the products of a chunk's rows and the
+ * weighted rows that kept states are sums of are carried in two bf16 parts (2^-16), and the result is rounded once.
+ * h_final and the gradient of h_init are sums in fp32 of unrounded values.  A row's NaN and infinities do not reach
+ * earlier rows; what they reach is not finite, but may be NaN where the definition has an infinity.
  */
 size_t lin_attn_fwd_workspace_bytes(int B, int S, int rows, int H, int G, int dk, int dv, mlstm_dtype dtype);
 size_t lin_attn_fwd_call_workspace_bytes(int B, int S, int rows, int H, int G, int dk, int dv, mlstm_dtype dtype,

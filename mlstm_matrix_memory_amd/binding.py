@@ -1166,6 +1166,7 @@ def lin_attn_fwd(q, k, v, log_decay, scale=None, h_init=None, seq_start=None, ma
     bound of the lengths) in one dtype, float32 or bfloat16, H a multiple of G; log_decay [H]
     float32, a constant; scale defaults to dk ** -0.5; h_init and h_final [B,H,dv,dk] float32 (None
     = zero).  Rows of o that belong to no sequence are not written: undefined unless o_out is given.
+    What a NaN or infinity reaches (no earlier row) is not finite: NaN also in place of an infinity.
     """
     import torch
     dev, code = _gpu(q, "q"), _dtype_code(q, "q")

@@ -17,7 +17,8 @@
 //
 // Rows of z later (backwards: earlier) than row i must not reach it, even where they are NaN or
 // infinite and their factor is zero.  Only slabs on the diagonal have such rows: there a
-// column's first such value is noted, and rows from it on become NaN.
+// column's first such value is noted, and rows from it on become NaN (also where the sum would be infinite:
+// the value's factors are gone by then).
 #include "lin_attn_common.h"
 
 namespace mlstm {

@@ -9,7 +9,8 @@
 // The state is held and returned in fp32, and its sums keep fp32's accuracy on bf16 instructions:
 // the weighted rows w y (fp32) are cut into three bf16 parts, 8 bits each, whose sum they are
 // exactly, and x is exact.  One part alone is 1.7e-3 off, two 2.7e-6.  Where only rounded states
-// leave the call two parts are taken.
+// leave the call two parts are taken.  (An infinite y is cut into an infinity and NaN, and an infinite x meets parts
+// that are zero: in bf16 both leave NaN where the sum is infinite.)
 //
 // Few tiles over long sequences are cut into segments: a first pass sums every segment from zero, a small
 // kernel runs along these sums and leaves in their places the states that enter the segments (and

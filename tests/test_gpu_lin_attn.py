@@ -302,3 +302,55 @@ def test_final_states_and_gradients_that_are_not_wanted(final, h, dh, grad_h, S,
     assert ("h_final" in got) == final and ("dh0" in got) == grad_h
     for n, x in got.items():
         ref.assert_within(n, x, *want[n])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+@pytest.mark.parametrize("name", ["q", "k"])
+def test_nan_and_infinities_in_later_rows_of_q_and_k(name, value, dtype):
+    """A value in a row of q or k reaches no earlier row of the output, nor rows, columns and heads of the gradients that do
+    not read it; rows that read it are not finite."""
+    import torch
+    from mlstm_matrix_memory_amd import lin_attn_bwd, lin_attn_fwd
+    announce(f"lin_attn with {value} in {name} {dtype}")
+    c = la.make(2, 200, 4, 2, 20, 72, dtype, seed=19, init=False)
+    clean = la.reference(c)
+    for row, col in ((0, 3), (37, 5), (63, 19), (130, 0), (199, 7)):
+        d = dict(c)
+        d[name] = c[name].copy()
+        d[name][row, 1, col] = value             # of the first sequence, and of the heads 2 and 3
+        t = on_gpu(d, False)
+        o, final = lin_attn_fwd(t["q"], t["k"], t["v"], t["g"], scale=c["scale"])
+        grads = lin_attn_bwd(t["q"], t["k"], t["v"], t["g"], t["do"], scale=c["scale"])
+        torch.cuda.synchronize()
+        got = {"o": to_np(o).reshape(c["v"].shape), "h_final": to_np(final)}
+        got.update((n, to_np(x).reshape(c[s].shape)) for n, x, s in zip(("dq", "dk", "dv"), grads, "qkv"))
+        hit = {n: np.zeros(x.shape, bool) for n, x in got.items()}
+        if name == "q":                          # o_row, dv and one column of dk up to the row
+            hit["o"][row, 2:], hit["dv"][:row + 1, 2:], hit["dk"][:row + 1, 1, col] = True, True, True
+        else:                                    # o and one column of dq from the row on, dv of the row, one column of the state
+            hit["o"][row:200, 2:], hit["dq"][row:200, 1, col], hit["dv"][row, 2:], hit["h_final"][0, 2:, :, col] = True, True, True, True
+        for n, x in got.items():
+            ref.assert_within(f"{n} row {row}", np.where(hit[n], 0, x), np.where(hit[n], 0, clean[n][0]), clean[n][1])
+            assert not np.isfinite(x[hit[n]]).any(), n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_states_behind_nan_and_infinities(dtype):
+    """Rows of the final state that a NaN or infinity of v reaches are not finite, the others as without it; through
+    chunks and segments."""
+    import torch
+    from mlstm_matrix_memory_amd import lin_attn_fwd
+    announce(f"lin_attn states behind NaN and infinities {dtype}")
+    for S in (90, 200, 1200):
+        c = la.make(1, S, 2, 1, 24, 40, dtype, seed=95, grads=False, decay=[-1e-3, -0.002])
+        clean = la.reference(c)
+        c["v"][S // 3, 0, 7], c["v"][S // 2, 1, 30] = np.inf, np.nan
+        t = on_gpu(c, False)
+        _, final = lin_attn_fwd(t["q"], t["k"], t["v"], t["g"], scale=c["scale"], h_init=t["h"])
+        torch.cuda.synchronize()
+        hit = np.zeros((1, 2, 40, 24), bool)
+        hit[0, 0, 7], hit[0, 1, 30] = True, True
+        final = to_np(final)
+        ref.assert_within("h", np.where(hit, 0, final), np.where(hit, 0, clean["h_final"][0]), clean["h_final"][1])
+        assert not np.isfinite(final[hit]).any()
