@@ -467,9 +467,11 @@ hipError_t tile_pick(const MmArgs& a, const MmShape& s) {
     const long long tiles128 = (long long)((a.M + 127) / 128) * ((a.N + 127) / 128);
     if (!aligned)
         return tiles128 >= 256 ? tile_launch<T, 2, 2, 4, 4, BLOCK, false>(a, s) : tile_launch<T, 2, 2, 2, 2, BLOCK, false>(a, s);
-    // 256 x 256 where that fills the chip (8192 x 8192 x 2048: 186 us, with 128 x 128 209), 64 x 64 where 128 x 128 does not
-    // (fp32 results keep to 128 x 128: their widened operands do not fit beside 256 x 256 accumulators)
-    if constexpr (sizeof(T) == 2) {
+    // 256 x 256 where that fills the chip (8192 x 8192 x 2048: 173 us, with 128 x 128 209), 64 x 64 where 128 x 128 does not
+    // (1536 x 1536 x 4096: 29.4 us, with 128 x 128 33.8; 2048 x 2048 x 2048 19.8 and 19.0).  Not 256 x 256 for scales of single rows,
+    // four factors a lane and tile: they spill 42 registers (8192 x 8192 x 2048: 330 us, with 128 x 128 201), nor for fp32
+    // results, whose widened operands do not fit beside the sums.
+    if constexpr (sizeof(T) == 2 && BLOCK) {
         const long long tiles256 = (long long)((a.M + 255) / 256) * ((a.N + 255) / 256);
         if (tiles256 >= 256) return tile_launch<T, 4, 2, 4, 8, BLOCK, true>(a, s);
     }
