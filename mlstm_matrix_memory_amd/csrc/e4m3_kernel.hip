@@ -465,8 +465,14 @@ template <typename T, bool BLOCK>
 hipError_t tile_pick(const MmArgs& a, const MmShape& s) {
     const bool aligned = a.K % 16 == 0 && a.K <= MM_ALIGNED_MAX_K && (((uintptr_t)a.a | (uintptr_t)a.b) & 15) == 0;
     const long long tiles128 = (long long)((a.M + 127) / 128) * ((a.N + 127) / 128);
-    if (!aligned)
-        return tiles128 >= 256 ? tile_launch<T, 2, 2, 4, 4, BLOCK, false>(a, s) : tile_launch<T, 2, 2, 2, 2, BLOCK, false>(a, s);
+    if (!aligned) {
+        // 3000 x 3000 x 2051, 128 x 128 against 64 x 64: bf16 67 us and 73; fp32, whose loads in flight then spill 12 to 25
+        // registers beside the widened operands, 116 and 77
+        if constexpr (sizeof(T) == 2) {
+            if (tiles128 >= 256) return tile_launch<T, 2, 2, 4, 4, BLOCK, false>(a, s);
+        }
+        return tile_launch<T, 2, 2, 2, 2, BLOCK, false>(a, s);
+    }
     // 256 x 256 where that fills the chip (8192 x 8192 x 2048: 173 us, with 128 x 128 209), 64 x 64 where 128 x 128 does not
     // (1536 x 1536 x 4096: 29.4 us, with 128 x 128 33.8; 2048 x 2048 x 2048 19.8 and 19.0).  Not 256 x 256 for scales of single rows,
     // four factors a lane and tile: they spill 42 registers (8192 x 8192 x 2048: 330 us, with 128 x 128 201), nor for fp32
