@@ -644,7 +644,8 @@ mlstm_status mlstm_quant_e4m3(const void* x, long long x_stride, int rows, int c
  * A linear layer y = x W^T in these terms, with W [N,K]: forward a = x, b = W (128 x 128); gradient
  * of x: a = dy, b = W transposed by the quantiser; gradient of W: a = dy transposed, b = x
  * transposed, both 1 x 128 (the blocks run over the rows of the batch).  A NaN or infinity in a
- * row of a or b, or in its scales, reaches that row or column of y and no other.
+ * row of a or b, or in its scales, reaches that row or column of y and no other (in a scale of 128 rows: their
+ * columns).
  */
 mlstm_status mlstm_mm_e4m3(const void* a, const float* a_scale, const void* b, const float* b_scale,
                            int block_rows, int M, int N, int K, mlstm_dtype out_dtype,

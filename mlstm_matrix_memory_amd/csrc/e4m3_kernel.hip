@@ -11,8 +11,8 @@
 // A block's inner products run on the matrix cores (16 x 16 x 128 e4m3, fp32 sums), and its scales
 // enter as one multiply-add per element and block, from registers: an instruction of 32 cycles is
 // followed by 4 multiply-adds of 4 cycles, which the other wave of the SIMD's matrix
-// instructions cover in part: 8192 x 8192 x 2048 takes 181 us (1.5 PFLOP/s), without them 143 of 186 traced,
-// without the loads 163.  b is the instruction's row operand, so that a lane holds four neighbouring
+// instructions cover in part: 8192 x 8192 x 2048 takes 183 us (1.5 PFLOP/s; traced 185, without the multiply-adds
+// 143, without the loads 163).  b is the instruction's row operand, so that a lane holds four neighbouring
 // columns of one row of y: one scale of a for them, and stores of four elements.
 #include "block_internal.h"
 #include "e4m3_common.h"
@@ -231,8 +231,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void mm_tile_kernel(MmShape s, T* 
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int wn = wave % WN, wm = wave / WN;
     // neighbouring workgroups go to different dies: each die takes a run of tiles, in bands of 8 tile rows of y, so
-    // that the 32 tiles it runs at once are about 8 x 4 and share rows of a and b in its L2 (down columns of y: 208 us
-    // against 186)
+    // that the 32 tiles it runs at once are about 8 x 4 and share rows of a and b in its L2 (down columns of y 208 us,
+    // so 186 then)
     const int m_tiles = (s.M + BM - 1) / BM, n_tiles = (s.N + BN - 1) / BN, tiles = m_tiles * n_tiles;
     const int per = (tiles + 7) / 8, id = (int)(blockIdx.x % 8) * per + blockIdx.x / 8;
     if (id >= tiles) return;
@@ -325,7 +325,9 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void mm_tile_kernel(MmShape s, T* 
             else sb[j] = *reinterpret_cast<const f32x4*>(&scales[buf][r + 4 * lg]);
         }
         // a row of tiles' matrix instructions beside the multiply-adds of the row before; the order is
-        // fixed, as the compiler's own kept every tile's products at once and spilled
+        // fixed, as the compiler's own kept every tile's products at once and spilled them.  256 x 256 still has 18
+        // registers too few: 76 bytes a lane go to scratch before the loop (40 of the 172 MB that 8192 x 8192 x 2048
+        // writes), addresses that only a last, shorter block reads again, and two values of the end.
         f32x4 p[2][NT];
         float sa[2];
         Fragment<T> fa = fragment(BN + 16 * MT * wm + lr);
@@ -369,7 +371,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void mm_tile_kernel(MmShape s, T* 
 }
 
 // ---- product: few rows of a ----------------------------------------------------------
-// (4 x 2048 x 4096: 6.2 us traced, 8.9 with the host's call.)
+// (4 x 2048 x 4096: 6.4 us traced, 9.1 with the host's call.)
 // A workgroup takes 16 rows of b and all of a (16 MT rows); its waves take every WAVES-th block and
 // load fragments as they are, with no LDS between: the time is that of b's bytes and of one
 // trip to HBM.  Their sums are added in wave order.
@@ -473,10 +475,11 @@ hipError_t tile_pick(const MmArgs& a, const MmShape& s) {
         }
         return tile_launch<T, 2, 2, 2, 2, BLOCK, false>(a, s);
     }
-    // 256 x 256 where that fills the chip (8192 x 8192 x 2048: 173 us, with 128 x 128 209), 64 x 64 where 128 x 128 does not
-    // (1536 x 1536 x 4096: 29.4 us, with 128 x 128 33.8; 2048 x 2048 x 2048 19.8 and 19.0).  Not 256 x 256 for scales of single rows,
-    // four factors a lane and tile: they spill 42 registers (8192 x 8192 x 2048: 330 us, with 128 x 128 201), nor for fp32
-    // results, whose widened operands do not fit beside the sums.
+    // 256 x 256 where that fills the chip (8192 x 8192 x 2048 164.5 us, with 128 x 128 182; 4096 x 4096 x 8192 140 and 173),
+    // 64 x 64 where 128 x 128 does not (1536 x 1536 x 4096 29 us, with 128 x 128 34; 2048 x 2048 x 2048 19.8 and 19.0; fp32 at
+    // 4096 x 4096 x 2048 88 and 75).  Not 256 x 256 for scales of single rows, four factors a lane and tile: they spill 42
+    // registers (8192 x 8192 x 2048 330 us, with 128 x 128 201), nor for fp32 results, whose widened operands do not fit
+    // beside the sums.
     if constexpr (sizeof(T) == 2 && BLOCK) {
         const long long tiles256 = (long long)((a.M + 255) / 256) * ((a.N + 255) / 256);
         if (tiles256 >= 256) return tile_launch<T, 4, 2, 4, 8, BLOCK, true>(a, s);

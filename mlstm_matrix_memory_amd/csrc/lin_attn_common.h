@@ -133,6 +133,8 @@ struct LaBatch {
 // behind each other), and a block lies as the instruction's lanes hold it: 16 x 16 tiles [dv][dk], of which
 // lane l has row l % 16, columns 4 (l / 16) .. + 3.  A tile is then one run of memory for the writer's
 // wave, whole lines (as rows of dk they were 32 bytes each, and HBM read what it was about to write).
+// In bf16 one part of a state is kept: results are then 2.1e-3 off, with two parts (hi and lo) 1.66e-3, their own rounding, but
+// the call of (1, 32768, 8 heads of 256) takes 575 us for 454, the backward of (4, 2048, 4 heads of 384) 445 for 333.
 struct LaStates {
     LaRows x, y;
     const float* init;                           // [B,H,dv,dk] or null

@@ -5,15 +5,15 @@
 //   out_i = state_factor e^{g n_i} (state a_i) + row_factor sum_j e^{g|i-j|} (a_i . y_j) z_j
 //
 // A workgroup of four waves has 64 rows i, a wave 16 of them for all of the kernel (32 a wave leave room for half
-// as many workgroups: 239 us against 206 at (1, 32768, 8 heads of 256)).  First it forms their products with all rows j of
+// as many workgroups: a sixth slower at (1, 32768, 8 heads of 256)).  First it forms their products with all rows j of
 // the chunk, transposed (j across the instruction's rows), so that a lane's results are already the
 // operand of the next product: decayed and masked, in bf16 cut into two parts, they stay in
 // registers.  Then, 64 columns of out at a time, the state's products with a, their decay, and
-// the products with z.  y, the state and z pass through LDS in slabs of 64 x 64, one ahead (two at a time: 231 us
-// against 236).
+// the products with z.  y, the state and z pass through LDS in slabs of 64 x 64, one ahead (two at a time, with the products
+// in one part: 231 us against 236).
 //
-// Bound by the slabs' way from HBM and L2: 236 us there for 0.69 GB read and 0.13 written, 3.5 TB/s; the waves wait for memory
-// 70% of their time, the matrix instructions take 12%.
+// Bound by the slabs' way from HBM and L2: 235 to 240 us there for 0.72 GB read and 0.13 written, 3.6 TB/s; the waves wait 68%
+// of their time, the matrix instructions take 13%.
 //
 // Rows of z later (backwards: earlier) than row i must not reach it, even where they are NaN or
 // infinite and their factor is zero.  Only slabs on the diagonal have such rows: there a
@@ -386,7 +386,8 @@ hipError_t launch(const LaBatch& b, const OutShape& s) {
 
 template <typename T, typename OT, bool BACK, bool COLS>
 hipError_t pick_held(const LaBatch& b, const OutShape& s) {
-    // a's slabs are held while registers last: (4, 2048, 4 heads of 384) 82 us with 6 read again and again, 50 held
+    // up to 6 of a's slabs are held: (4, 2048, 4 heads of 384) 82 us with 6 read again and again, 50 held.  Wider heads
+    // read theirs for every slab (6 take 174 to 184 of 256 registers; more were not built)
     if (s.da % 8 || s.dz % 8) return launch<T, OT, 0, BACK, COLS, false>(b, s);
     if (s.da <= 64) return launch<T, OT, 1, BACK, COLS, true>(b, s);
     if (s.da <= 128) return launch<T, OT, 2, BACK, COLS, true>(b, s);

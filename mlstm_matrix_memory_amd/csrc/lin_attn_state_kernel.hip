@@ -18,8 +18,9 @@
 // pass then has to be exact.  (Second pass with three parts, its segments joined by the readers: 186 us at
 // (1, 32768, 8 heads of 256), now 129.)
 //
-// Bound there by the 64 turns between two barriers, 2 us each: without the parts' arithmetic 112 us of 122, without the
-// matrix instructions 90, with every block read again 125.  Kept as rows of dk, the states' stores of 32
+// Bound there by the 64 turns between two barriers, 2 us each: without the parts' arithmetic 112 us of 122 (an earlier first
+// pass; now 133), without the matrix instructions 90, with every block read again 125.  At 128 x 256 the passes spill
+// up to 16 registers.  Kept as rows of dk, the states' stores of 32
 // bytes made HBM read the lines first: 323 us against 230.
 #include <type_traits>
 
@@ -359,7 +360,11 @@ Tile tile_of(const LaBatch& b, int dk, int dv) {
 }  // namespace
 
 // Sequences are cut where their tiles leave the chip idle, into segments of at least 2 chunks (2 against 4: 15 us a pass
-// against 22 over 3158 rows of 8 heads of 96).
+// against 22 over 3158 rows of 8 heads of 96), from 8 chunks on: with 8, cut and whole take 60 and 80 us at 4 heads of 256, 46
+// and 58 at 4 sequences of 6 heads of 96, the whole backward of the 3158 rows 125 and 137; with 6, 59 and 67, 47 and 48,
+// but in fp32 70 and 61, backwards 178 and 157, and 75 and 63 over 3948 packed rows of 6 heads of 40 x 77.  A packed batch counts as
+// B sequences of S rows: one long sequence among many short ones is not cut (8192 rows of 4 heads of 128 alone 54 us,
+// with 63 sequences of 64 rows 342).
 int la_segment_rows(const LaBatch& b, int dk, int dv) {
     const Tile t = tile_of(b, dk, dv);
     const long long tiles = (long long)((dk + t.k - 1) / t.k) * ((dv + t.v - 1) / t.v) * b.H * b.B;
